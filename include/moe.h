@@ -59,7 +59,12 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_ROUTER_SOFTMAX = 0, MOE_ROUTER_SIGMOID_GROUPED = 1 } moe_router_kind;
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+/* The layer's hidden states are F32 or BF16; the token operators at the end of this header
+ * also take F16, and E4M3 where they say so. */
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2, MOE_DT_E4M3 = 3 } moe_dtype;
+/* Activation of moe_linear (GELU: the exact form, with erf). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3,
+               MOE_ACT_SWIGLU = 4 } moe_act;
 
 /* Layer shape and routing options. */
 typedef struct {
@@ -285,6 +290,84 @@ int moe_debug_wait_timeout(void *ws, size_t ws_bytes, int iterations, void *stre
  * Returns MOE_ERR_INVALID_ARG before any launch when an argument is out of range. */
 int moe_residual_rmsnorm(int T, int H, float *resid, const float *add, const uint16_t *x0,
                          float eps, uint16_t *x_next, void *stream);
+
+/* ------------------------------------------------------------------ token operators
+ * What a user's own layers need around the experts: 8-bit rows out of the norm, tokens
+ * sorted by expert and back (with gradients), and a matrix product that takes those rows.
+ * They need no config, no packed blob and no workspace, allocate nothing and may be captured
+ * into a graph.  Rows are contiguous in their last dimension; `ld*` is the distance between
+ * rows in elements.  Pointers are aligned to their element unless stated otherwise; faster
+ * paths are taken where rows start on 16-byte boundaries.  The pages have no counterpart. */
+
+/* RMS norm with the residual's addition and 8-bit output:
+ *   r = x + add (rounded to dtype; add may be NULL), stored to resid (NULL: not stored),
+ *   y = r * weight / sqrt(mean(r^2) + eps)           (weight [H] of dtype, NULL = ones;
+ *                                                     normalize = 0: y = r * weight),
+ *   for each group of `group` elements of the row (32, 64, 128 or 256, the last group may be
+ *   shorter; 0 = the whole row): scale = max|y| / 448, q = e4m3(y * 448 / max|y|), to nearest.
+ * x, add, resid [T][H] of dtype (F32, BF16, F16), q [T][H] e4m3 codes, scale
+ * [T][ceil(H / group)] fp32, contiguous.  The norm is taken of the rounded r; sums are fp32
+ * (squares that overflow fp32 give y = 0).  A group whose largest |y| is below 2^-100 gets
+ * scale 0 and codes 0; one that holds a NaN or an infinity gets a NaN or infinite scale.
+ * resid may be x or add (same ld).  With normalize = 0 it quantises rows as they are: weights
+ * or hidden activations for moe_linear.  1 <= H <= 32768 (else MOE_ERR_UNSUPPORTED). */
+int moe_rmsnorm_e4m3(int T, int H, const void *x, long ldx, moe_dtype dtype, const void *add,
+                     long ldadd, const void *weight, float eps, int normalize, int group,
+                     void *resid, long ldr, uint8_t *q, long ldq, float *scale, void *stream);
+
+/* Order the T * k slots by (expert, slot): ids [T][k] as moe_route_topk writes them.
+ * offsets [E+1]: first row of each expert (offsets[E] = rows in all); perm [T*k]: slot
+ * t*k+j of each row; slot_pos [T][k]: row of each slot.  Ids outside [0, E) are dropped:
+ * slot_pos -1, and perm ends in as many -1.  The order is stable, ids of one token may
+ * repeat.  k <= 16, E <= 256, T <= 65535 (these operators: else MOE_ERR_UNSUPPORTED). */
+int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *offsets,
+                    int32_t *perm, int32_t *slot_pos, void *stream);
+
+/* xs[slot_pos[t][j]] = x[t]: rows of T * k, those past offsets[n_experts] zero.  x [T][H] and
+ * xs [T*k][H] of any moe_dtype, moved as they are.  n_scales > 0: the rows' scales move along,
+ * scale [T][n_scales] -> scale_s [T*k][n_scales] fp32. */
+int moe_dispatch_rows(int T, int k, int n_experts, int H, moe_dtype dtype, const void *x, long ldx,
+                      const int32_t *slot_pos, const int32_t *offsets, void *xs, int n_scales,
+                      const float *scale, long ldscale, float *scale_s, void *stream);
+
+/* out[t] = add[t] + sum over j with slot_pos[t][j] >= 0 of w[t][j] * y[slot_pos[t][j]], summed
+ * in slot order in fp32 and rounded once.  y [T*k][H] (F32, BF16, F16), w [T][k] fp32 (NULL =
+ * ones), out [T][H] of y's type or F32, add [T][H] of out's type or NULL; out may be add. */
+int moe_combine_rows(int T, int k, int H, const void *y, moe_dtype y_dtype,
+                     const int32_t *slot_pos, const float *w, const void *add, long ldadd,
+                     void *out, long ldout, moe_dtype out_dtype, void *stream);
+
+/* Gradient of moe_combine_rows: dy[slot_pos[t][j]] = w[t][j] * dout[t] (rows past
+ * offsets[n_experts] zero), dw[t][j] = <dout[t], y[slot_pos[t][j]]> (fp32, 0 for a dropped
+ * slot; the order of its sum is fixed).  The gradient of add is dout itself. */
+int moe_combine_rows_grad(int T, int k, int n_experts, int H, moe_dtype dtype, const void *dout,
+                          long lddout, const void *y, const int32_t *slot_pos,
+                          const int32_t *offsets, const float *w, void *dy, float *dw,
+                          void *stream);
+
+/* Gradient of moe_dispatch_rows: dx[t] = sum over the slots of t of dxs[slot_pos[t][j]]. */
+int moe_dispatch_rows_grad(int T, int k, int H, moe_dtype dtype, const void *dxs,
+                           const int32_t *slot_pos, void *dx, long lddx, moe_dtype dx_dtype,
+                           void *stream);
+
+/* Matrix product with its epilogue, dense or by expert:
+ *   z = (sum_k x[r][k] w[e][n][k]) * x_scale[r] * w_scale[e][n] + bias[e][n]
+ *   out[r][n] = act(z) + residual[r][n]
+ * x [R][K], w [E][N][K] contiguous, both of dtype (E4M3, BF16 or F16); x_scale [R], w_scale
+ * and bias [E][N] fp32, each may be NULL; residual and out [R][N] of out_dtype (F32, BF16,
+ * F16), residual may be NULL or out itself (same ld).  n_experts = 0: dense, w [N][K], offsets
+ * unused.  Else rows [offsets[e], offsets[e+1]) use expert e (device memory, as
+ * moe_sort_tokens writes it; values are clamped to [0, R] and to ascending order); rows of no
+ * expert get zeros and are not read.  act = SWIGLU: w has 2 N rows per expert (gate rows, then
+ * up rows; w_scale and bias too) and out = silu(z_gate) * z_up + residual.
+ * Accumulation is fp32 on the tensor cores.  x, w and x's rows 16-byte aligned; K a multiple
+ * of 16, N of 16 for SWIGLU, E <= 256, else MOE_ERR_UNSUPPORTED.  status: optional device
+ * int32, set to MOE_ERR_TIMEOUT if a bounded wait gave up (the output is then undefined), else
+ * left as it is. */
+int moe_linear(int R, int N, int K, int n_experts, const void *x, long ldx, moe_dtype dtype,
+               const float *x_scale, const void *w, const float *w_scale, const float *bias,
+               moe_act act, const void *residual, long ldres, const int32_t *offsets, void *out,
+               long ldout, moe_dtype out_dtype, int32_t *status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,204 @@
+// norm_e4m3.cu -- residual addition, RMS norm and 8-bit rows with scales in one pass.
+//
+// For each token: r = round(x + add) (the residual stream, in x's type), m = mean(r^2),
+// y = r w / sqrt(m + eps); then for each group of G elements (or the whole row)
+// a = max |y|, scale = a / 448 and q = e4m3(y * 448 / a), 448 being the largest e4m3 value.
+// The statistics are fp32.  The largest |y| of a group is the largest |r w| times the row's
+// factor, so the sum of squares and the maxima come out of the same single reduction and
+// every element is read from memory once: the row stays in registers between the reduction
+// and the encoding.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "dev.cuh"
+#include "elem.cuh"
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kE4m3Tiny = 0x1p-100f;  // smaller maxima give scale 0 and codes 0: 448 / a is finite
+
+struct NormArgs {
+  const void *x, *add, *w;
+  void *resid;
+  uint8_t *q;
+  float *scale;
+  long ldx, ldadd, ldr, ldq;
+  int T, H, group, normalize;
+  float eps;
+};
+
+// scale and factor of a group whose largest |y| is `a`; NaN and infinity pass into the scale
+__device__ __forceinline__ float e4m3_factor(float a, float &scale) {
+  if (a < kE4m3Tiny) {
+    scale = 0.f;
+    return 0.f;
+  }
+  scale = __fdiv_rn(a, kE4m3Max);
+  return __fdiv_rn(kE4m3Max, a);
+}
+
+// TPR threads per row (a multiple of 32, blockDim.x); ROWS > 1 only with one warp per row.
+// Thread t holds the packs t, t + TPR, ... (at most PACKS of them).  Maxima are taken on the
+// bit patterns of |v|, where NaN is largest, so a NaN shows in the scale.
+template <typename T, int PACKS, bool VEC>
+__global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(const NormArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int tpr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.T) return;  // whole rows leave together (blockDim.y > 1: a row is one warp)
+  const T *x = (const T *)a.x + (size_t)t * a.ldx;
+  const T *add = a.add ? (const T *)a.add + (size_t)t * a.ldadd : nullptr;
+  T *resid = a.resid ? (T *)a.resid + (size_t)t * a.ldr : nullptr;
+  const T *w = (const T *)a.w;
+  const int H = a.H;
+
+  Pack<T> px[PACKS], pa[PACKS];
+#pragma unroll
+  for (int j = 0; j < PACKS; j++) {
+    const int i = 8 * (tid + j * tpr);
+    if (i < H) {
+      px[j] = load_pack<T, VEC>(x, i, H);
+      if (add) pa[j] = load_pack<T, VEC>(add, i, H);
+    }
+  }
+  float v[PACKS][8];
+  uint32_t mx[PACKS];
+  float ss = 0.f;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < PACKS; j++) {
+    const int i = 8 * (tid + j * tpr);
+    mx[j] = 0;
+    if (i >= H) continue;
+    if (add) {
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        px[j].v[k] = Elem<T>::put(Elem<T>::get(px[j].v[k]) + Elem<T>::get(pa[j].v[k]));
+    }
+    if (resid) store_pack<T, VEC>(resid, i, H, px[j]);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      v[j][k] = Elem<T>::get(px[j].v[k]);
+      ss += v[j][k] * v[j][k];
+    }
+    if (w) {
+      const Pack<T> pw = load_pack<T, VEC>(w, i, H);
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[j][k] *= Elem<T>::get(pw.v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) mx[j] = max(mx[j], __float_as_uint(fabsf(v[j][k])));
+    m = max(m, mx[j]);
+  }
+  ss = warp_sum(ss);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (tpr > 32) {
+    __shared__ float ps[32];
+    __shared__ uint32_t pm[32];
+    if (lane == 0) ps[warp] = ss, pm[warp] = m;
+    __syncthreads();
+    const int nw = tpr >> 5;
+    ss = warp_sum(lane < nw ? ps[lane] : 0.f);
+    m = __reduce_max_sync(0xffffffffu, lane < nw ? pm[lane] : 0u);
+  }
+  const float inv = a.normalize ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
+  const int G = a.group, ng = G ? (H + G - 1) / G : 1;
+  float *scale = a.scale + (size_t)t * ng;
+  float f, s;
+  if (!G) {
+    f = e4m3_factor(__uint_as_float(m) * inv, s);
+    if (tid == 0) scale[0] = s;
+  }
+  uint8_t *q = a.q + (size_t)t * a.ldq;
+#pragma unroll
+  for (int j = 0; j < PACKS; j++) {
+    const int i = 8 * (tid + j * tpr);
+    if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
+      uint32_t gm = mx[j];
+      for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+      f = e4m3_factor(__uint_as_float(gm) * inv, s);
+      if (i < H && i % G == 0) scale[i / G] = s;
+    }
+    if (i >= H) continue;
+    uint16_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
+      c[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    }
+    if (VEC) {
+      *(uint2 *)(q + i) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        if (i + k < H) q[i + k] = (uint8_t)(c[k >> 1] >> (8 * (k & 1)));
+    }
+  }
+}
+
+template <typename T, bool VEC>
+static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
+  const int packs = (a.H + 7) / 8;
+  if (packs <= 128) {  // one warp a row, four rows a CTA: nothing to exchange between warps
+    const dim3 grid((a.T + 3) / 4), block(32, 4);
+    if (packs <= 32) return launch_pdl(rmsnorm_e4m3_kernel<T, 1, VEC>, grid, block, 0, st, a);
+    if (packs <= 64) return launch_pdl(rmsnorm_e4m3_kernel<T, 2, VEC>, grid, block, 0, st, a);
+    return launch_pdl(rmsnorm_e4m3_kernel<T, 4, VEC>, grid, block, 0, st, a);
+  }
+  // few rows: as many threads as the row has packs (shortest path through one row); many
+  // rows: up to four packs a thread (more loads in flight a thread, fewer threads to join)
+  const int want = a.T <= 2 * dev_info().sms ? 1 : 4;
+  auto threads = [&](int p) { return ((packs + p - 1) / p + 31) / 32 * 32; };
+  const int per = want == 1 && threads(1) <= 1024   ? 1
+                  : want == 1 && threads(2) <= 1024 ? 2
+                  : threads(4) <= 512               ? 4
+                                                    : 8;
+  const dim3 grid(a.T), block(threads(per));
+  if (per == 1) return launch_pdl(rmsnorm_e4m3_kernel<T, 1, VEC>, grid, block, 0, st, a);
+  if (per == 2) return launch_pdl(rmsnorm_e4m3_kernel<T, 2, VEC>, grid, block, 0, st, a);
+  if (per == 4) return launch_pdl(rmsnorm_e4m3_kernel<T, 4, VEC>, grid, block, 0, st, a);
+  return launch_pdl(rmsnorm_e4m3_kernel<T, 8, VEC>, grid, block, 0, st, a);
+}
+
+template <typename T>
+static cudaError_t launch_norm_t(const NormArgs &a, cudaStream_t st) {
+  const uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.add | (uintptr_t)a.w | (uintptr_t)a.resid |
+                      (uintptr_t)(a.ldx * sizeof(T)) | (uintptr_t)(a.ldadd * sizeof(T)) |
+                      (uintptr_t)(a.ldr * sizeof(T));
+  const bool vec = p % 16 == 0 && a.H % 8 == 0 && ((uintptr_t)a.q | (uintptr_t)a.ldq) % 8 == 0;
+  return vec ? launch_norm<T, true>(a, st) : launch_norm<T, false>(a, st);
+}
+
+}  // namespace moe
+
+extern "C" int moe_rmsnorm_e4m3(int T, int H, const void *x, long ldx, moe_dtype dtype,
+                                const void *add, long ldadd, const void *weight, float eps,
+                                int normalize, int group, void *resid, long ldr, uint8_t *q,
+                                long ldq, float *scale, void *stream) {
+  if (T < 0 || H <= 0 || !(eps >= 0.f) || (normalize != 0 && normalize != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16 && dtype != MOE_DT_F16)
+    return MOE_ERR_INVALID_ARG;
+  if (H > 32768) return MOE_ERR_UNSUPPORTED;
+  if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const uintptr_t es = dtype == MOE_DT_F32 ? 4 : 2;
+  if (!x || !q || !scale || ldx < H || ldq < H || (add && ldadd < H) || (resid && ldr < H))
+    return MOE_ERR_INVALID_ARG;
+  if ((uintptr_t)x % es || (uintptr_t)add % es || (uintptr_t)weight % es ||
+      (uintptr_t)resid % es || (uintptr_t)scale % 4)
+    return MOE_ERR_INVALID_ARG;
+  const moe::NormArgs a{x, add, weight, resid, q, scale, ldx, add ? ldadd : 0, resid ? ldr : 0,
+                        ldq, T, H, group, normalize, eps};
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == MOE_DT_F32    ? moe::launch_norm_t<float>(a, st)
+                        : dtype == MOE_DT_BF16 ? moe::launch_norm_t<__nv_bfloat16>(a, st)
+                                               : moe::launch_norm_t<__half>(a, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -1,0 +1,504 @@
+// tokens.cu -- tokens sorted by expert and back, with weights applied, and the gradients.
+//
+// The routed rows of T tokens with k slots each are ordered by (expert, slot):
+//   sort      slot_pos[t][j] = position of slot (t, j), perm = its inverse, offsets[E+1]
+//   dispatch  xs[slot_pos[t][j]] = x[t]
+//   combine   out[t] = add[t] + sum_j w[t][j] y[slot_pos[t][j]]
+//   gradients dy[slot_pos[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[slot_pos[t][j]]>,
+//             dx[t] = sum_j dxs[slot_pos[t][j]]
+// Everything but the sort is bound by memory traffic; all of it is organised by token, so a
+// token's row is read (or written) once for its k slots, and every sum has one fixed order:
+// no atomics touch a result.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "dev.cuh"
+#include "elem.cuh"
+#include "moe_internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+
+// ------------------------------------------------------------------------------- sort
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxE = 256;
+constexpr int kSortCluster = 8;
+
+// A stable counting sort in one launch: one CTA, or a cluster of eight for long id arrays.
+// Each warp owns a contiguous run of slots and counts it into its own row of `hist`
+// (lanes with equal ids are found by match_any, so no atomics); the rows are scanned over
+// the warps, the CTA totals over the cluster (distributed shared memory), the expert totals
+// over the experts; then each warp walks its run again and hands out positions in order.
+__global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E, const int32_t *ids,
+                                                                   int32_t *offsets, int32_t *perm,
+                                                                   int32_t *slot_pos) {
+  __shared__ int hist[kSortWarps][kSortMaxE + 1];
+  __shared__ int total[kSortMaxE];   // this CTA's slots per expert
+  __shared__ int start[kSortMaxE + 1];
+  cg::cluster_group cl = cg::this_cluster();
+  const int ncta = cl.num_blocks(), rank = cl.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned below = (1u << lane) - 1u;
+  pdl_wait();
+  pdl_trigger();
+  const int runs = ncta * kSortWarps;
+  const int len = ((n + runs - 1) / runs + 31) / 32 * 32;  // slots per warp
+  const long lo = min((long)n, (long)(rank * kSortWarps + warp) * len);
+  const long hi = min((long)n, lo + len);
+  for (int e = lane; e < E; e += 32) hist[warp][e] = 0;
+  __syncwarp();
+  for (long i0 = lo; i0 < hi; i0 += 32) {
+    const long i = i0 + lane;
+    int e = i < hi ? ids[i] : -1;
+    if (e >= E) e = -1;
+    if (e < 0) e = -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && (peers & below) == 0) hist[warp][e] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) {  // exclusive scan over the warps
+    int s = 0;
+    for (int w = 0; w < kSortWarps; w++) {
+      const int c = hist[w][e];
+      hist[w][e] = s;
+      s += c;
+    }
+    total[e] = s;
+  }
+  cl.sync();
+  for (int e = tid; e < E; e += blockDim.x) {
+    int before = 0, all = 0;
+    for (int c = 0; c < ncta; c++) {
+      const int v = cl.map_shared_rank(total, c)[e];
+      if (c < rank) before += v;
+      all += v;
+    }
+    start[e] = all;
+    for (int w = 0; w < kSortWarps; w++) hist[w][e] += before;
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive scan over the experts
+    const int per = (E + 31) / 32;
+    int s = 0;
+    for (int i = 0; i < per; i++)
+      if (lane * per + i < E) s += start[lane * per + i];
+    int incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int r = incl - s;
+    for (int i = 0; i < per; i++) {
+      const int e = lane * per + i;
+      if (e < E) {
+        const int c = start[e];
+        start[e] = r;
+        r += c;
+      }
+    }
+    if (lane == 31) start[E] = incl;
+  }
+  __syncthreads();
+  for (long i0 = lo; i0 < hi; i0 += 32) {
+    const long i = i0 + lane;
+    int e = i < hi ? ids[i] : -1;
+    if (e >= E) e = -1;
+    if (e < 0) e = -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    int pos = -1;
+    if (e >= 0) pos = start[e] + hist[warp][e] + __popc(peers & below);
+    __syncwarp();
+    if (e >= 0 && (peers & below) == 0) hist[warp][e] += __popc(peers);
+    __syncwarp();
+    if (i < hi) slot_pos[i] = pos;
+    if (pos >= 0) perm[pos] = (int32_t)i;
+  }
+  // dropped slots leave a tail without rows
+  for (long p = (long)start[E] + rank * kSortThreads + tid; p < n; p += (long)ncta * kSortThreads)
+    perm[p] = -1;
+  if (rank == 0)
+    for (int e = tid; e <= E; e += blockDim.x) offsets[e] = start[e];
+  cl.sync();  // no CTA leaves while another may still read its totals
+}
+
+// ----------------------------------------------------------------------- row movement
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+
+// Row copies move `U` units of W bytes a lane per step, all loads before the stores.
+template <typename W>
+__global__ void __launch_bounds__(kRowThreads)
+    dispatch_kernel(int T, int k, int E, long units, long ldx, const W *x, const int32_t *slot_pos,
+                    const int32_t *offsets, W *xs, int pieces, int SC, const float *sc, long ldsc,
+                    float *scs) {
+  constexpr int U = 8;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long n = (long)T * k;
+  const long nwarps = (long)gridDim.x * kRowWarps;
+  const long gw = (long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  for (long item = gw; item < (long)T * pieces; item += nwarps) {
+    const long t = item / pieces;
+    const int piece = (int)(item - t * pieces);
+    const int my = lane < k ? slot_pos[t * k + lane] : -1;
+    const W *src = x + t * ldx;
+    for (long u0 = (long)piece * 32 * U; u0 < units; u0 += (long)pieces * 32 * U) {
+      W v[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const long i = u0 + u * 32 + lane;
+        if (i < units) v[u] = src[i];
+      }
+      for (int j = 0; j < k; j++) {
+        const int p = __shfl_sync(0xffffffffu, my, j);
+        if (p < 0 || p >= n) continue;
+        W *dst = xs + (long)p * units;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const long i = u0 + u * 32 + lane;
+          if (i < units) dst[i] = v[u];
+        }
+      }
+    }
+    if (piece == 0 && sc)
+      for (int j = 0; j < k; j++) {
+        const int p = __shfl_sync(0xffffffffu, my, j);
+        if (p < 0 || p >= n) continue;
+        for (int i = lane; i < SC; i += 32) scs[(long)p * SC + i] = sc[t * ldsc + i];
+      }
+  }
+  // rows without a slot are zero
+  const long live = min(n, (long)max(0, offsets[E]));
+  for (long p = live + gw; p < n; p += nwarps) {
+    W zero = {};
+    for (long i = lane; i < units; i += 32) xs[p * units + i] = zero;
+    if (sc)
+      for (int i = lane; i < SC; i += 32) scs[p * SC + i] = 0.f;
+  }
+}
+
+struct CombineArgs {
+  const void *y, *add;
+  const int32_t *slot_pos;
+  const float *w;
+  void *out;
+  long ldadd, ldout;
+  int T, k, H, packs;
+};
+
+// A thread per pack of eight elements of a token's row: k loads in flight (eight at a time),
+// fp32 sum in slot order, one rounding.
+template <typename TY, typename TO, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const CombineArgs a) {
+  constexpr int U = 8;
+  pdl_wait();
+  pdl_trigger();
+  const long item = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long t = item / a.packs;
+  if (t >= a.T) return;
+  const int i = 8 * (int)(item - t * a.packs);
+  const long n = (long)a.T * a.k;
+  const TY *y = (const TY *)a.y;
+  float acc[8];
+  if (a.add) {
+    const Pack<TO> p = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
+#pragma unroll
+    for (int m = 0; m < 8; m++) acc[m] = Elem<TO>::get(p.v[m]);
+  } else {
+#pragma unroll
+    for (int m = 0; m < 8; m++) acc[m] = 0.f;
+  }
+  for (int j0 = 0; j0 < a.k; j0 += U) {
+    int pos[U];
+    Pack<TY> v[U];
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      pos[j] = j0 + j < a.k ? a.slot_pos[t * a.k + j0 + j] : -1;
+      if (pos[j] >= n) pos[j] = -1;
+      if (pos[j] >= 0) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
+    }
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      if (pos[j] < 0) continue;
+      const float w = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
+#pragma unroll
+      for (int m = 0; m < 8; m++) acc[m] = fmaf(w, Elem<TY>::get(v[j].v[m]), acc[m]);
+    }
+  }
+  Pack<TO> o;
+#pragma unroll
+  for (int m = 0; m < 8; m++) o.v[m] = Elem<TO>::put(acc[m]);
+  store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i, a.H, o);
+}
+
+struct GradArgs {
+  const void *dout, *y;
+  const int32_t *slot_pos, *offsets;
+  const float *w;
+  void *dy;
+  float *dw;
+  long lddout;
+  int T, k, E, H;
+};
+
+// A CTA per token: its dout pack stays in registers for the k slots (KC of them at a time),
+// whose y rows are read for dw and whose dy rows are written.  dw is summed over lanes, then
+// over warps, in a fixed order.  CTAs past the tokens write the zero rows of the tail.
+template <typename T, bool VEC, int KC>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float part[KC][kRowWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long n = (long)a.T * a.k;
+  T *dy = (T *)a.dy;
+  if ((int)blockIdx.x >= a.T) {
+    const long live = min(n, (long)max(0, a.offsets[a.E]));
+    Pack<T> zero;
+#pragma unroll
+    for (int m = 0; m < 8; m++) zero.v[m] = Elem<T>::put(0.f);
+    for (long p = live + (blockIdx.x - a.T); p < n; p += gridDim.x - a.T)
+      for (int i = 8 * tid; i < a.H; i += 8 * blockDim.x)
+        store_pack<T, VEC>(dy + p * a.H, i, a.H, zero);
+    return;
+  }
+  const long t = blockIdx.x;
+  const T *dout = (const T *)a.dout + t * a.lddout;
+  const T *y = (const T *)a.y;
+  for (int j0 = 0; j0 < a.k; j0 += KC) {
+    int pos[KC];
+    float w[KC], acc[KC];
+#pragma unroll
+    for (int j = 0; j < KC; j++) {
+      const bool in = j0 + j < a.k;
+      pos[j] = in ? a.slot_pos[t * a.k + j0 + j] : -1;
+      if (pos[j] >= n) pos[j] = -1;
+      w[j] = in ? a.w ? a.w[t * a.k + j0 + j] : 1.0f : 0.f;
+      acc[j] = 0.f;
+    }
+    for (int i = 8 * tid; i < a.H; i += 8 * blockDim.x) {
+      const Pack<T> pd = load_pack<T, VEC>(dout, i, a.H);
+      Pack<T> py[KC];
+#pragma unroll
+      for (int j = 0; j < KC; j++)
+        if (pos[j] >= 0) py[j] = load_pack<T, VEC>(y + (long)pos[j] * a.H, i, a.H);
+      float d[8];
+#pragma unroll
+      for (int m = 0; m < 8; m++) d[m] = Elem<T>::get(pd.v[m]);
+#pragma unroll
+      for (int j = 0; j < KC; j++) {
+        if (pos[j] < 0) continue;
+        Pack<T> o;
+#pragma unroll
+        for (int m = 0; m < 8; m++) {
+          acc[j] = fmaf(d[m], Elem<T>::get(py[j].v[m]), acc[j]);
+          o.v[m] = Elem<T>::put(w[j] * d[m]);
+        }
+        store_pack<T, VEC>(dy + (long)pos[j] * a.H, i, a.H, o);
+      }
+    }
+    if (j0) __syncthreads();  // the last slots' sums have been read
+#pragma unroll
+    for (int j = 0; j < KC; j++) {
+      const float s = warp_sum(acc[j]);
+      if (lane == 0) part[j][warp] = s;
+    }
+    __syncthreads();
+    if (tid < KC && j0 + tid < a.k) {
+      float s = 0.f;
+      for (int q = 0; q < (int)blockDim.x / 32; q++) s += part[tid][q];
+      a.dw[t * a.k + j0 + tid] = s;
+    }
+  }
+}
+
+template <typename TY, typename TO>
+static cudaError_t launch_combine_rows(const CombineArgs &a0, cudaStream_t st) {
+  CombineArgs a = a0;
+  a.packs = (a.H + 7) / 8;
+  const uintptr_t p = (uintptr_t)a.y | (uintptr_t)a.add | (uintptr_t)a.out |
+                      (uintptr_t)(a.ldadd * sizeof(TO)) | (uintptr_t)(a.ldout * sizeof(TO));
+  const bool vec = p % 16 == 0 && a.H % 8 == 0;
+  const dim3 grid((unsigned)(((long)a.T * a.packs + kRowThreads - 1) / kRowThreads));
+  return vec ? launch_pdl(combine_rows_kernel<TY, TO, true>, grid, dim3(kRowThreads), 0, st, a)
+             : launch_pdl(combine_rows_kernel<TY, TO, false>, grid, dim3(kRowThreads), 0, st, a);
+}
+
+template <typename T, bool VEC>
+static cudaError_t launch_grad(const GradArgs &a, cudaStream_t st) {
+  const int packs = (a.H + 7) / 8;
+  const dim3 block(std::min(kRowThreads, (packs + 31) / 32 * 32));
+  const dim3 grid(a.T + std::min(a.T, 2 * dev_info().sms));
+  if (a.k <= 2) return launch_pdl(combine_grad_kernel<T, VEC, 2>, grid, block, 0, st, a);
+  return launch_pdl(combine_grad_kernel<T, VEC, 4>, grid, block, 0, st, a);
+}
+
+template <typename T>
+static cudaError_t launch_grad_t(const GradArgs &a, cudaStream_t st) {
+  const uintptr_t p = (uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy |
+                      (uintptr_t)(a.lddout * sizeof(T));
+  return p % 16 == 0 && a.H % 8 == 0 ? launch_grad<T, true>(a, st) : launch_grad<T, false>(a, st);
+}
+
+static bool float_type(int dt) {
+  return dt == MOE_DT_F32 || dt == MOE_DT_BF16 || dt == MOE_DT_F16;
+}
+static uintptr_t type_size(int dt) {
+  return dt == MOE_DT_F32 ? 4 : dt == MOE_DT_E4M3 ? 1 : 2;
+}
+
+// T and k as everywhere in the library; a row of H elements
+static int check_tokens(int T, int k) {
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (k < 1 || k > 16 || T > 65535) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+template <typename W>
+static cudaError_t launch_dispatch(int T, int k, int E, long row_bytes, long ldx_bytes,
+                                   const void *x, const int32_t *slot_pos, const int32_t *offsets,
+                                   void *xs, int SC, const float *sc, long ldsc, float *scs,
+                                   cudaStream_t st) {
+  const long units = row_bytes / (long)sizeof(W);
+  // few tokens: a row is shared by several warps, so that the copies spread over the SMs
+  const long chunks = std::max(1l, (units + 255) / 256);
+  const long target = 16l * dev_info().sms;
+  const int pieces = (int)std::min(chunks, std::max(1l, target / T));
+  const long items = (long)T * pieces;
+  const unsigned grid = (unsigned)std::min((items + kRowWarps - 1) / kRowWarps,
+                                           (long)dev_info().sms * 64);
+  return launch_pdl(dispatch_kernel<W>, dim3(std::max(1u, grid)), dim3(kRowThreads), 0, st, T, k,
+                    E, units, ldx_bytes / (long)sizeof(W), (const W *)x, slot_pos, offsets,
+                    (W *)xs, pieces, SC, sc, ldsc, scs);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *offsets,
+                    int32_t *perm, int32_t *slot_pos, void *stream) {
+  if (int r = check_tokens(T, k)) return r;
+  if (n_experts < 1 || n_experts > kSortMaxE) return MOE_ERR_UNSUPPORTED;
+  if (!offsets || (T && (!ids || !perm || !slot_pos))) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)perm | (uintptr_t)slot_pos) % 4)
+    return MOE_ERR_INVALID_ARG;
+  const int n = T * k;
+  // a warp walks its run 32 slots at a time: past two steps a warp, eight CTAs
+  const int ctas = n <= kSortThreads * 2 ? 1 : kSortCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, sort_tokens_kernel, n, n_experts, ids, offsets, perm, slot_pos) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_dispatch_rows(int T, int k, int n_experts, int H, moe_dtype dtype, const void *x, long ldx,
+                      const int32_t *slot_pos, const int32_t *offsets, void *xs, int n_scales,
+                      const float *scale, long ldscale, float *scale_s, void *stream) {
+  if (int r = check_tokens(T, k)) return r;
+  if (!float_type(dtype) && dtype != MOE_DT_E4M3) return MOE_ERR_INVALID_ARG;
+  if (H <= 0 || n_scales < 0 || n_experts < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const uintptr_t es = type_size(dtype);
+  if (!x || !xs || !slot_pos || !offsets || ldx < H) return MOE_ERR_INVALID_ARG;
+  if (n_scales && (!scale || !scale_s || ldscale < n_scales)) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)x | (uintptr_t)xs) % es || ((uintptr_t)slot_pos | (uintptr_t)offsets) % 4 ||
+      ((uintptr_t)scale | (uintptr_t)scale_s) % 4)
+    return MOE_ERR_INVALID_ARG;
+  const long row = (long)H * es, ld = ldx * (long)es;
+  const uintptr_t al = (uintptr_t)x | (uintptr_t)xs | (uintptr_t)row | (uintptr_t)ld;
+  const float *sc = n_scales ? scale : nullptr;
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  // the widest unit that every row's start and length allow
+  if (al % 16 == 0)
+    e = launch_dispatch<uint4>(T, k, n_experts, row, ld, x, slot_pos, offsets, xs, n_scales, sc,
+                               ldscale, scale_s, st);
+  else if (al % 4 == 0)
+    e = launch_dispatch<uint32_t>(T, k, n_experts, row, ld, x, slot_pos, offsets, xs, n_scales, sc,
+                                  ldscale, scale_s, st);
+  else if (al % 2 == 0)
+    e = launch_dispatch<uint16_t>(T, k, n_experts, row, ld, x, slot_pos, offsets, xs, n_scales, sc,
+                                  ldscale, scale_s, st);
+  else
+    e = launch_dispatch<uint8_t>(T, k, n_experts, row, ld, x, slot_pos, offsets, xs, n_scales, sc,
+                                 ldscale, scale_s, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_combine_rows(int T, int k, int H, const void *y, moe_dtype y_dtype,
+                     const int32_t *slot_pos, const float *w, const void *add, long ldadd,
+                     void *out, long ldout, moe_dtype out_dtype, void *stream) {
+  if (int r = check_tokens(T, k)) return r;
+  if (H <= 0 || !float_type(y_dtype) || !float_type(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != y_dtype && out_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const uintptr_t ey = type_size(y_dtype), eo = type_size(out_dtype);
+  if (!y || !slot_pos || !out || ldout < H || (add && ldadd < H)) return MOE_ERR_INVALID_ARG;
+  if ((uintptr_t)y % ey || ((uintptr_t)out | (uintptr_t)add) % eo ||
+      ((uintptr_t)slot_pos | (uintptr_t)w) % 4)
+    return MOE_ERR_INVALID_ARG;
+  const CombineArgs a{y, add, slot_pos, w, out, add ? ldadd : 0, ldout, T, k, H, 0};
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  if (y_dtype == MOE_DT_F32)
+    e = launch_combine_rows<float, float>(a, st);
+  else if (y_dtype == MOE_DT_BF16)
+    e = out_dtype == MOE_DT_F32 ? launch_combine_rows<__nv_bfloat16, float>(a, st)
+                                : launch_combine_rows<__nv_bfloat16, __nv_bfloat16>(a, st);
+  else
+    e = out_dtype == MOE_DT_F32 ? launch_combine_rows<__half, float>(a, st)
+                                : launch_combine_rows<__half, __half>(a, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_combine_rows_grad(int T, int k, int n_experts, int H, moe_dtype dtype, const void *dout,
+                          long lddout, const void *y, const int32_t *slot_pos,
+                          const int32_t *offsets, const float *w, void *dy, float *dw,
+                          void *stream) {
+  if (int r = check_tokens(T, k)) return r;
+  if (H <= 0 || n_experts < 0 || !float_type(dtype)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const uintptr_t es = type_size(dtype);
+  if (!dout || !y || !slot_pos || !offsets || !dy || !dw || lddout < H) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy) % es ||
+      ((uintptr_t)slot_pos | (uintptr_t)offsets | (uintptr_t)w | (uintptr_t)dw) % 4)
+    return MOE_ERR_INVALID_ARG;
+  const GradArgs a{dout, y, slot_pos, offsets, w, dy, dw, lddout, T, k, n_experts, H};
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == MOE_DT_F32    ? launch_grad_t<float>(a, st)
+                        : dtype == MOE_DT_BF16 ? launch_grad_t<__nv_bfloat16>(a, st)
+                                               : launch_grad_t<__half>(a, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_dispatch_rows_grad(int T, int k, int H, moe_dtype dtype, const void *dxs,
+                           const int32_t *slot_pos, void *dx, long lddx, moe_dtype dx_dtype,
+                           void *stream) {
+  return moe_combine_rows(T, k, H, dxs, dtype, slot_pos, nullptr, nullptr, 0, dx, lddx, dx_dtype,
+                          stream);
+}
+
+}  // extern "C"
