@@ -56,6 +56,7 @@ struct LinBars {
   uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort_flag;
+  alignas(16) float xs[4][kLinMaxN];  // token scales of the epilogue warps' tile
   int pre[kLinMaxE + 1];   // row tiles before each expert
   int off[kLinMaxE + 1];   // first row of each expert
 };
@@ -289,14 +290,33 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const bool in = f < a.N;
       const float sw = a.w_scale && in ? a.w_scale[(long)t.e * rows + wr] : 1.f;
       const float bi = a.bias && in ? a.bias[(long)t.e * rows + wr] : 0.f;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
+      // the tile's token scales, a copy per warp (1 where there are none, 0 past the rows)
+      float *xs = b->xs[quad];
+      __syncwarp();
+      for (int c = lane; c < a.BN; c += 32)
+        xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
+      __syncwarp();
+      if (!__all_sync(0xffffffffu,
+                      tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
         break;
       tc::fence_after_sync();
       const uint32_t taddr = tbase + buf * kLinMaxN + ((uint32_t)(32 * quad) << 16);
+      // of two columns, the lower lanes of a SwiGLU warp finish the first, the upper the second
+      const int up = GATED && lane >= 16;
+      TO *op = out + (long)(t.r0 + up) * a.ldout + f;
+      const TO *rp = res ? res + (long)(t.r0 + up) * a.ldres + f : nullptr;
       for (int c0 = 0; c0 < t.n; c0 += 16) {
+        constexpr int S = GATED ? 2 : 1, J = 16 / S;
+        float y[J], rv[J];
         uint32_t v[16];
         __syncwarp();
         tc::tmem_ld16(taddr + c0, v);
+        const int left = in ? t.n - c0 - up : 0;  // columns that this lane stores
+        if (rp) {
+#pragma unroll
+          for (int j = 0; j < J; j++)
+            rv[j] = S * j < left ? Elem<TO>::get(rp[(c0 + S * j) * a.ldres]) : 0.f;
+        }
         tc::tmem_wait_ld();
         if (c0 + 16 >= t.n) {  // the accumulator is read: the next tile may use it
           tc::fence_before_sync();
@@ -304,35 +324,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) tc::mbar_arrive(&b->acc_empty[buf]);
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += GATED ? 2 : 1) {
-          if (c0 + j >= t.n) break;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 s4 = *(const float4 *)(xs + c0 + j);
+          const float z0 = fmaf(__uint_as_float(v[j]) * s4.x, sw, bi);
+          const float z1 = fmaf(__uint_as_float(v[j + 1]) * s4.y, sw, bi);
+          const float z2 = fmaf(__uint_as_float(v[j + 2]) * s4.z, sw, bi);
+          const float z3 = fmaf(__uint_as_float(v[j + 3]) * s4.w, sw, bi);
           if (GATED) {
-            // two columns at once: the lower lanes finish the first, the upper the second
-            const long r = t.r0 + c0 + j;
-            const bool two = c0 + j + 1 < t.n;
-            const float s0 = a.x_scale ? a.x_scale[r] : 1.f;
-            const float s1 = a.x_scale && two ? a.x_scale[r + 1] : 1.f;
-            const float z0 = fmaf(__uint_as_float(v[j]) * s0, sw, bi);
-            const float z1 = fmaf(__uint_as_float(v[j + 1]) * s1, sw, bi);
-            const bool up = lane >= 16;
-            const float other = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
-            const float g = up ? other : z0, u = up ? z1 : other;
-            float y = silu_f(g) * u;
-            const long ro = r + (up ? 1 : 0);
-            if (in && (!up || two)) {
-              if (res) y += Elem<TO>::get(res[ro * a.ldres + f]);
-              out[ro * a.ldout + f] = Elem<TO>::put(y);
-            }
+            const float o0 = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
+            const float o1 = __shfl_xor_sync(0xffffffffu, up ? z2 : z3, 16);
+            y[j / 2] = up ? silu_f(o0) * z1 : silu_f(z0) * o0;
+            y[j / 2 + 1] = up ? silu_f(o1) * z3 : silu_f(z2) * o1;
           } else {
-            const long r = t.r0 + c0 + j;
-            const float sx = a.x_scale ? a.x_scale[r] : 1.f;
-            float y = lin_act(fmaf(__uint_as_float(v[j]) * sx, sw, bi), a.act);
-            if (in) {
-              if (res) y += Elem<TO>::get(res[r * a.ldres + f]);
-              out[r * a.ldout + f] = Elem<TO>::put(y);
-            }
+            y[j] = z0, y[j + 1] = z1, y[j + 2] = z2, y[j + 3] = z3;
           }
         }
+        if (!GATED && a.act != MOE_ACT_NONE) {
+#pragma unroll
+          for (int j = 0; j < J; j++) y[j] = lin_act(y[j], a.act);
+        }
+        if (rp) {
+#pragma unroll
+          for (int j = 0; j < J; j++) y[j] += rv[j];
+        }
+#pragma unroll
+        for (int j = 0; j < J; j++)
+          if (S * j < left) op[(c0 + S * j) * a.ldout] = Elem<TO>::put(y[j]);
       }
       if (buf) bph ^= 1;
       buf ^= 1;
