@@ -20,6 +20,8 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "dev.cuh"
 #include "elem.cuh"
@@ -29,13 +31,23 @@
 
 namespace moe {
 
-constexpr int kLinM = 128;         // weight rows per tile
+constexpr int kLinM = 128;         // weight rows per CTA and tile
 constexpr int kLinMaxN = 256;      // token rows per tile
 constexpr int kLinStages = 12;     // ring slots at most
 constexpr int kLinMaxE = 256;
 constexpr int kLinThreads = 192;
 constexpr int kLinRing = 208 * 1024;  // shared memory of the ring
 constexpr long kLinWaitNs = 2000000000L;
+
+// How CTAs share a tile:
+//   kOne    one CTA a tile, persistent.
+//   kPair   two CTAs (the two SMs of a TPC) a tile of 256 weight rows: each loads its own 128
+//           weight rows and half of the token rows, and the leader issues MMAs of M = 256 that
+//           read both halves, so token rows cross from L2 once for 256 weight rows.
+//   kSplit  a cluster of up to eight CTAs a tile, each over a part of K, not persistent: the
+//           partial sums are exchanged through distributed shared memory and added in rank
+//           order, each CTA finishing a share of the columns.
+enum LinMode { kOne = 0, kPair = 1, kSplit = 2 };
 
 struct LinArgs {
   const float *x_scale, *w_scale, *bias;
@@ -47,7 +59,8 @@ struct LinArgs {
   int R, N, E;       // E = 0: dense
   int KB, ke;        // k-blocks, elements per k-block
   int BN, stages;    // token rows per tile, ring slots
-  int FT;            // feature tiles
+  int FT;            // feature tiles (of 128 weight rows, kPair: 256)
+  int split;         // kSplit: CTAs per tile
   int act;
   int kind8, bf16;   // operand type: e4m3, or bf16 / fp16
 };
@@ -61,30 +74,106 @@ struct LinBars {
   int off[kLinMaxE + 1];   // first row of each expert
 };
 
-__device__ __forceinline__ void mma_ss_f8(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// ---------------------------------------------------------------- pairs and clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z,
-                                            uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
-      : "memory");
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ void tma_load_5d(void *dst, const void *tmap, int x, int y, int z, int u,
-                                            int v, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(tc::smem_u32(bar))
-      : "memory");
+// the address of a shared-memory object in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+  return r;
 }
+__device__ __forceinline__ void arrive_in_cta(uint64_t *bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   in_cta(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void store_in_cta(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void lin_tmem_alloc(uint32_t *dst) {  // whole warp, all 512 columns
+  if (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     tc::smem_u32(dst))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tc::tmem_alloc<512>(dst);
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void lin_tmem_free(uint32_t t) {
+  if (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+  else
+    tc::tmem_dealloc<512>(t);
+}
+
+// one MMA: 32 bytes of K (32 e4m3 or 16 16-bit elements); PAIR: over both CTAs' tiles
+template <bool PAIR, bool KIND8>
+__device__ __forceinline__ void lin_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                        uint32_t accumulate) {
+#define LIN_MMA(GROUP, KIND)                                                              \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                          \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" \
+               ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(accumulate) : "memory")
+  if (PAIR) {
+    if (KIND8) LIN_MMA("2", "f8f6f4"); else LIN_MMA("2", "f16");
+  } else {
+    if (KIND8) LIN_MMA("1", "f8f6f4"); else LIN_MMA("1", "f16");
+  }
+#undef LIN_MMA
+}
+
+// arrive on `bar` (PAIR: in both CTAs) once the MMAs issued so far have completed
+template <bool PAIR>
+__device__ __forceinline__ void lin_commit(uint64_t *bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc::mma_commit(bar);
+}
+
+// TMA loads into this CTA's ring; `bar` is a shared::cluster address (PAIR: the leader's)
+#define LIN_TMA(DIMS, COORDS, ...)                                                             \
+  if (PAIR)                                                                                    \
+    asm volatile("cp.async.bulk.tensor." DIMS                                                  \
+                 ".shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "     \
+                 "[%0], [%1, " COORDS "], [%2];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(bar), \
+                 __VA_ARGS__ : "memory");                                                      \
+  else                                                                                         \
+    asm volatile("cp.async.bulk.tensor." DIMS                                                  \
+                 ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "                  \
+                 "[%0], [%1, " COORDS "], [%2];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(bar), \
+                 __VA_ARGS__ : "memory")
+template <bool PAIR>
+__device__ __forceinline__ void lin_load_2d(void *dst, const void *map, uint32_t bar, int x, int y) {
+  LIN_TMA("2d", "{%3, %4}", "r"(x), "r"(y));
+}
+template <bool PAIR>
+__device__ __forceinline__ void lin_load_3d(void *dst, const void *map, uint32_t bar, int x, int y,
+                                            int z) {
+  LIN_TMA("3d", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
+}
+template <bool PAIR>
+__device__ __forceinline__ void lin_load_5d(void *dst, const void *map, uint32_t bar, int x, int u,
+                                            int v) {
+  LIN_TMA("5d", "{%3, %4, %4, %5, %6}", "r"(x), "r"(0), "r"(u), "r"(v));
+}
+#undef LIN_TMA
 
 // A tile: rows [r0, r0 + n) of expert e, feature tile ft.  Row tiles run fastest, so that
 // CTAs working at the same time share weight tiles in L2.
@@ -117,15 +206,97 @@ __device__ __forceinline__ float lin_act(float z, int act) {
   }
 }
 
+// What a lane of an epilogue warp needs to turn accumulator values of its weight row into
+// outputs: scales, bias, and where its columns go.
 template <typename TO, bool GATED>
+struct LinOut {
+  float sw, bi;
+  const float *xs;   // token scales of the tile
+  TO *op;
+  const TO *rp;
+  long ldout, ldres;
+  int cols;          // columns of the tile that this lane stores (0: its feature is past N)
+  int up, act;       // of two columns, the lower lanes of a SwiGLU warp finish the first,
+                     // the upper lanes the second
+
+  __device__ __forceinline__ LinOut(const LinArgs &a, const LinTile &t, int ft128, int row,
+                                    const float *xs_)
+      : xs(xs_), ldout(a.ldout), ldres(a.ldres), act(a.act) {
+    const int lane = row & 31;
+    int wr, f;  // this lane's weight row, and the output feature it (and its partner) give
+    up = GATED && lane >= 16;
+    if (GATED) {
+      f = ft128 * 64 + (row >> 5) * 16 + (lane & 15);
+      wr = f + (up ? a.N : 0);
+    } else {
+      wr = f = ft128 * kLinM + row;
+    }
+    const bool in = f < a.N;
+    const long wi = (long)t.e * (GATED ? 2 * a.N : a.N) + wr;
+    sw = a.w_scale && in ? a.w_scale[wi] : 1.f;
+    bi = a.bias && in ? a.bias[wi] : 0.f;
+    op = (TO *)a.out + (long)(t.r0 + up) * ldout + f;
+    rp = a.residual ? (const TO *)a.residual + (long)(t.r0 + up) * ldres + f : nullptr;
+    cols = in ? t.n - up : 0;
+  }
+
+  static constexpr int S = GATED ? 2 : 1, J = 16 / S;
+
+  // the residual of columns c0 .. c0 + 15, loaded ahead of the accumulator's wait
+  __device__ __forceinline__ void prefetch(int c0, int end, float (&rv)[J]) const {
+    if (!rp) return;
+    const int left = min(cols, end - up) - c0;
+#pragma unroll
+    for (int j = 0; j < J; j++)
+      rv[j] = S * j < left ? Elem<TO>::get(rp[(c0 + S * j) * ldres]) : 0.f;
+  }
+
+  // accumulator values v of columns c0 .. c0 + 15 (c0 a multiple of 4; columns at `end` and
+  // beyond are left out): scale, bias, activation, residual, store
+  __device__ __forceinline__ void finish(int c0, int end, const float (&v)[16],
+                                         const float (&rv)[J]) const {
+    float y[J];
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 s4 = *(const float4 *)(xs + c0 + j);
+      const float z0 = fmaf(v[j] * s4.x, sw, bi), z1 = fmaf(v[j + 1] * s4.y, sw, bi);
+      const float z2 = fmaf(v[j + 2] * s4.z, sw, bi), z3 = fmaf(v[j + 3] * s4.w, sw, bi);
+      if (GATED) {
+        const float o0 = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
+        const float o1 = __shfl_xor_sync(0xffffffffu, up ? z2 : z3, 16);
+        y[j / S] = up ? silu_f(o0) * z1 : silu_f(z0) * o0;
+        y[j / S + 1] = up ? silu_f(o1) * z3 : silu_f(z2) * o1;
+      } else {
+        y[j % J] = z0, y[(j + 1) % J] = z1, y[(j + 2) % J] = z2, y[(j + 3) % J] = z3;
+      }
+    }
+    if (!GATED && act != MOE_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < J; j++) y[j] = lin_act(y[j], act);
+    }
+    if (rp) {
+#pragma unroll
+      for (int j = 0; j < J; j++) y[j] += rv[j];
+    }
+    const int left = min(cols, end - up) - c0;
+#pragma unroll
+    for (int j = 0; j < J; j++)
+      if (S * j < left) op[(c0 + S * j) * ldout] = Elem<TO>::put(y[j]);
+  }
+};
+
+template <typename TO, bool GATED, int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                   const LinArgs a) {
+  constexpr bool PAIR = MODE == kPair, SPLIT = MODE == kSplit;
   extern __shared__ uint8_t smraw[];
   uint8_t *ring = tc::align_smem_1024(smraw);
-  const int stage_bytes = (kLinM + a.BN) * 128;
+  const int xrows = PAIR ? a.BN / 2 : a.BN;  // token rows in this CTA's stages
+  const int stage_bytes = (kLinM + xrows) * 128;
   LinBars *b = (LinBars *)(ring + kLinRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = MODE == kOne ? 0 : cluster_rank();
   if (tid == 0) {
     for (int s = 0; s < a.stages; s++) {
       tc::mbar_init(&b->full[s], 1);
@@ -133,15 +304,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&b->acc_full[i], 1);
-      tc::mbar_init(&b->acc_empty[i], 4);
+      tc::mbar_init(&b->acc_empty[i], PAIR ? 8 : 4);
     }
     tc::mbar_init(&b->drain, 1);
     b->abort_flag = 0;
     tc::fence_barrier_init();
   }
+  __syncwarp();
   // tensor memory before the trigger: a successor may start as soon as every CTA has
   // triggered, and must not take columns that this grid still has to allocate
-  if (warp == 0) tc::tmem_alloc<512>(&b->tmem);
+  if (warp == 0) lin_tmem_alloc<PAIR>(&b->tmem);
   pdl_wait();
   pdl_trigger();
   // the experts' rows, clamped to [0, R] and kept in order, so that no offset leads out of x
@@ -178,44 +350,61 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if (MODE == kOne) __syncthreads(); else cluster_sync();  // barriers are ready in every CTA
   tc::fence_after_sync();
   const uint32_t tbase = b->tmem;
   volatile int *abort = &b->abort_flag;
   auto give_up = [&]() {
     *abort = 1;
+    if (PAIR)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(&b->abort_flag, rank ^ 1)),
+                   "r"(1)
+                   : "memory");
     if (a.status) *a.status = MOE_ERR_TIMEOUT;
   };
+  // the tiles of this CTA (pair, cluster), and its part of K
   const int total = b->pre[max(1, a.E)] * a.FT;
+  const int cta = PAIR ? blockIdx.x / 2 : SPLIT ? blockIdx.x / a.split : blockIdx.x;
+  const int ctas = PAIR ? gridDim.x / 2 : SPLIT ? gridDim.x / a.split : gridDim.x;
+  const int kb0 = SPLIT ? (int)((long)a.KB * rank / a.split) : 0;
+  const int kb1 = SPLIT ? (int)((long)a.KB * (rank + 1) / a.split) : a.KB;
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------- producer
       bool ok = true;
-      uint32_t it = 0, armed = 0, last_ph = 0;
+      uint32_t armed = 0, last_ph = 0;
       int s = 0;
       uint32_t ph = 0;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = cta; tile < total && ok; tile += ctas) {
         const LinTile t = lin_tile(a, b, tile);
-        for (int kb = 0; kb < a.KB; kb++, it++) {
+        const int ft = PAIR ? 2 * t.ft + rank : t.ft;
+        // the pair's MMAs take the first half of the columns from the leader
+        const int row = t.r0 + (PAIR ? (int)rank * (round16(t.n) / 2) : 0);
+        for (int kb = kb0; kb < kb1; kb++) {
           if (!tc::mbar_wait(&b->empty[s], ph ^ 1, abort, kLinWaitNs)) { ok = false; break; }
           uint8_t *st = ring + (size_t)s * stage_bytes;
-          tc::mbar_arrive_expect_tx(&b->full[s], stage_bytes);
+          const uint32_t bar = PAIR ? in_cta(&b->full[s], 0) : tc::smem_u32(&b->full[s]);
+          if (rank == 0 || !PAIR) {
+            tc::mbar_arrive_expect_tx(&b->full[s], PAIR ? 2 * stage_bytes : stage_bytes);
+            armed |= 1u << s;
+            last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          }
           if (GATED)
-            tma_load_5d(st, &wmap, kb * a.ke, 0, 0, t.ft * (kLinM / 32), t.e, &b->full[s]);
+            lin_load_5d<PAIR>(st, &wmap, bar, kb * a.ke, ft * (kLinM / 32), t.e);
           else
-            tma_load_3d(st, &wmap, kb * a.ke, t.ft * kLinM, t.e, &b->full[s]);
-          tc::tma_load_2d(st + kLinM * 128, &xmap, kb * a.ke, t.r0, &b->full[s]);
-          armed |= 1u << s;
-          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+            lin_load_3d<PAIR>(st, &wmap, bar, kb * a.ke, ft * kLinM, t.e);
+          lin_load_2d<PAIR>(st + kLinM * 128, &xmap, bar, kb * a.ke, row);
           if (++s == a.stages) s = 0, ph ^= 1;
         }
       }
-      // every copy started lands before the CTA exits
-      if (!ok) {
+      if (!ok) {  // every copy started lands before the CTA exits
         give_up();
         for (int q = 0; q < a.stages; q++)
           if ((armed >> q) & 1) wait_nofail(&b->full[q], (last_ph >> q) & 1, kLinWaitNs);
+        // the second CTA of a pair has no barrier of its own to wait on: its copies are loads
+        // of some microseconds
+        if (PAIR && rank) for (int i = 0; i < 1000; i++) __nanosleep(1000);
       }
     }
   } else if (warp == 1) {
@@ -224,16 +413,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     bool ok = true, issued = false;
     int s = 0, buf = 0;
     uint32_t ph = 0, bph = 0;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    for (int tile = cta; tile < total && ok && (!PAIR || rank == 0); tile += ctas) {
       const LinTile t = lin_tile(a, b, tile);
-      const uint32_t idesc = tc::idesc_f16(a.bf16, round16(t.n));
+      const uint32_t idesc = tc::idesc_f16(a.bf16, round16(t.n)) +
+                             (PAIR ? (uint32_t)(kLinM >> 4) << 24 : 0u);  // M = 256
       int got = 1;
       if (leader) got = tc::mbar_wait(&b->acc_empty[buf], bph ^ 1, abort, kLinWaitNs);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t d = tbase + buf * kLinMaxN;
-      for (int kb = 0; kb < a.KB; kb++) {
+      for (int kb = kb0; kb < kb1; kb++) {
         if (leader) got = tc::mbar_wait_spin(&b->full[s], ph, abort, kLinWaitNs);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
@@ -244,20 +434,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (a.kind8) {
 #pragma unroll
             for (int kk = 0; kk < 4; kk++)
-              mma_ss_f8(d, da + 2 * kk, db + 2 * kk, idesc, (kb | kk) != 0);
+              lin_mma<PAIR, true>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > kb0) | (kk != 0));
           } else {
 #pragma unroll
             for (int kk = 0; kk < 4; kk++)
-              tc::mma_ss(d, da + 2 * kk, db + 2 * kk, idesc, (kb | kk) != 0);
+              lin_mma<PAIR, false>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > kb0) | (kk != 0));
           }
-          tc::mma_commit(&b->empty[s]);
+          lin_commit<PAIR>(&b->empty[s]);
         }
         __syncwarp();
         issued = true;
         if (++s == a.stages) s = 0, ph ^= 1;
       }
       if (!ok) break;
-      if (leader) tc::mma_commit(&b->acc_full[buf]);
+      if (leader) lin_commit<PAIR>(&b->acc_full[buf]);
       __syncwarp();
       if (buf) bph ^= 1;
       buf ^= 1;
@@ -265,110 +455,122 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (leader && !ok) {
       give_up();
       if (issued) {  // every MMA issued completes before the tensor memory is freed
-        tc::mma_commit(&b->drain);
+        lin_commit<PAIR>(&b->drain);
         wait_nofail(&b->drain, 0, kLinWaitNs);
       }
     }
-  } else {
+  } else if (!SPLIT) {
     // -------------------------------------------------- epilogue: a lane per weight row
     const int quad = warp & 3;  // the warp's quarter of the tensor-memory lanes
-    const int rows = GATED ? 2 * a.N : a.N;
-    const TO *res = (const TO *)a.residual;
-    TO *out = (TO *)a.out;
+    float *xs = b->xs[quad];
     int buf = 0;
     uint32_t bph = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    for (int tile = cta; tile < total; tile += ctas) {
       const LinTile t = lin_tile(a, b, tile);
-      // this lane's weight row, and the output feature that it (and its partner) give
-      int wr, f;
-      if (GATED) {
-        f = t.ft * 64 + quad * 16 + (lane & 15);
-        wr = f + (lane >= 16 ? a.N : 0);
-      } else {
-        wr = f = t.ft * kLinM + quad * 32 + lane;
-      }
-      const bool in = f < a.N;
-      const float sw = a.w_scale && in ? a.w_scale[(long)t.e * rows + wr] : 1.f;
-      const float bi = a.bias && in ? a.bias[(long)t.e * rows + wr] : 0.f;
       // the tile's token scales, a copy per warp (1 where there are none, 0 past the rows)
-      float *xs = b->xs[quad];
       __syncwarp();
       for (int c = lane; c < a.BN; c += 32)
         xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
       __syncwarp();
+      const LinOut<TO, GATED> o(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad * 32 + lane, xs);
       if (!__all_sync(0xffffffffu,
                       tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
         break;
       tc::fence_after_sync();
       const uint32_t taddr = tbase + buf * kLinMaxN + ((uint32_t)(32 * quad) << 16);
-      // of two columns, the lower lanes of a SwiGLU warp finish the first, the upper the second
-      const int up = GATED && lane >= 16;
-      TO *op = out + (long)(t.r0 + up) * a.ldout + f;
-      const TO *rp = res ? res + (long)(t.r0 + up) * a.ldres + f : nullptr;
       for (int c0 = 0; c0 < t.n; c0 += 16) {
-        constexpr int S = GATED ? 2 : 1, J = 16 / S;
-        float y[J], rv[J];
         uint32_t v[16];
+        float f[16], rv[LinOut<TO, GATED>::J];
         __syncwarp();
         tc::tmem_ld16(taddr + c0, v);
-        const int left = in ? t.n - c0 - up : 0;  // columns that this lane stores
-        if (rp) {
-#pragma unroll
-          for (int j = 0; j < J; j++)
-            rv[j] = S * j < left ? Elem<TO>::get(rp[(c0 + S * j) * a.ldres]) : 0.f;
-        }
+        o.prefetch(c0, t.n, rv);
         tc::tmem_wait_ld();
         if (c0 + 16 >= t.n) {  // the accumulator is read: the next tile may use it
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&b->acc_empty[buf]);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 s4 = *(const float4 *)(xs + c0 + j);
-          const float z0 = fmaf(__uint_as_float(v[j]) * s4.x, sw, bi);
-          const float z1 = fmaf(__uint_as_float(v[j + 1]) * s4.y, sw, bi);
-          const float z2 = fmaf(__uint_as_float(v[j + 2]) * s4.z, sw, bi);
-          const float z3 = fmaf(__uint_as_float(v[j + 3]) * s4.w, sw, bi);
-          if (GATED) {
-            const float o0 = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
-            const float o1 = __shfl_xor_sync(0xffffffffu, up ? z2 : z3, 16);
-            y[j / 2] = up ? silu_f(o0) * z1 : silu_f(z0) * o0;
-            y[j / 2 + 1] = up ? silu_f(o1) * z3 : silu_f(z2) * o1;
-          } else {
-            y[j] = z0, y[j + 1] = z1, y[j + 2] = z2, y[j + 3] = z3;
+          if (lane == 0) {
+            if (PAIR) arrive_in_cta(&b->acc_empty[buf], 0);
+            else tc::mbar_arrive(&b->acc_empty[buf]);
           }
         }
-        if (!GATED && a.act != MOE_ACT_NONE) {
 #pragma unroll
-          for (int j = 0; j < J; j++) y[j] = lin_act(y[j], a.act);
-        }
-        if (rp) {
-#pragma unroll
-          for (int j = 0; j < J; j++) y[j] += rv[j];
-        }
-#pragma unroll
-        for (int j = 0; j < J; j++)
-          if (S * j < left) op[(c0 + S * j) * a.ldout] = Elem<TO>::put(y[j]);
+        for (int j = 0; j < 16; j++) f[j] = __uint_as_float(v[j]);
+        o.finish(c0, t.n, f, rv);
       }
       if (buf) bph ^= 1;
       buf ^= 1;
     }
-    // rows of no expert are zero
-    if (a.E) {
-      const long live0 = b->off[a.E], lead = b->off[0];
-      const long first = (long)blockIdx.x * 128 + (warp - 2) * 32 + lane;
-      const long step = (long)gridDim.x * 128;
-      for (long i = first; i < lead * a.N; i += step)
-        out[i / a.N * a.ldout + i % a.N] = Elem<TO>::put(0.f);
-      for (long i = first; i < (a.R - live0) * a.N; i += step)
-        out[(live0 + i / a.N) * a.ldout + i % a.N] = Elem<TO>::put(0.f);
+  }
+  if (SPLIT) {
+    // ---------------------------------------------------- a tile's partial sums, joined
+    // A cluster has at most one tile.  Column c belongs to CTA c / cpc; once every CTA's MMAs
+    // are done its ring holds the partial sums [from CTA][own column][weight row].
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const bool work = cta < total;
+    const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
+    float *xs = b->xs[quad];
+    bool ok = work;
+    LinTile t{};
+    if (work) t = lin_tile(a, b, cta);
+    if (warp >= 2 && work) {
+      for (int c = lane; c < a.BN; c += 32)
+        xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_backoff(&b->acc_full[0], 0, abort, kLinWaitNs, 32));
+      tc::fence_after_sync();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && ok) {
+      const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16);
+      for (int c0 = 0; c0 < t.n; c0 += 16) {
+        uint32_t v[16];
+        __syncwarp();
+        tc::tmem_ld16(taddr + c0, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+          const int to = (c0 + j) / cpc, c = c0 + j - to * cpc;
+          if (c0 + j < t.n)
+            store_in_cta(in_cta(ring, to) + (uint32_t)(((rank * cpc + c) * kLinM + row) * 4),
+                         __uint_as_float(v[j]));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && ok) {
+      const LinOut<TO, GATED> o(a, t, t.ft, row, xs);
+      const float *part = (const float *)ring;
+      const int c1 = min(t.n, (int)(rank + 1) * cpc);
+      for (int c0 = rank * cpc; c0 < c1; c0 += 16) {
+        float f[16], rv[LinOut<TO, GATED>::J];
+        o.prefetch(c0, c1, rv);
+#pragma unroll
+        for (int j = 0; j < 16; j++) f[j] = 0.f;
+        for (int q = 0; q < a.split; q++)
+#pragma unroll
+          for (int j = 0; j < 16; j++)
+            if (c0 + j < c1) f[j] += part[(q * cpc + c0 + j - (int)rank * cpc) * kLinM + row];
+        o.finish(c0, c1, f, rv);
+      }
     }
   }
+  // rows of no expert are zero
+  if (a.E && warp >= 2) {
+    const long tail = b->off[a.E], lead = b->off[0];
+    const long first = (long)blockIdx.x * 128 + (warp - 2) * 32 + lane;
+    const long step = (long)gridDim.x * 128;
+    TO *out = (TO *)a.out;
+    for (long i = first; i < lead * a.N; i += step)
+      out[i / a.N * a.ldout + i % a.N] = Elem<TO>::put(0.f);
+    for (long i = first; i < (a.R - tail) * a.N; i += step)
+      out[(tail + i / a.N) * a.ldout + i % a.N] = Elem<TO>::put(0.f);
+  }
+  __syncwarp();
   tc::fence_before_sync();
-  __syncthreads();
+  if (MODE == kOne) __syncthreads(); else cluster_sync();  // nobody still uses a peer's memory
   tc::fence_after_sync();
-  if (warp == 0) tc::tmem_dealloc<512>(tbase);
+  if (warp == 0) lin_tmem_free<PAIR>(tbase);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
@@ -383,33 +585,122 @@ static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
   return fn;
 }
 
-// Token rows per tile: the fewest tiles of at most 256 rows, all of about the same size; by
-// expert the mean number of rows decides (an expert's last tile costs only what it has).
-static int lin_bn(int R, int E) {
-  const int m = E ? (R + E - 1) / E : R;
-  if (E) return m >= 96 ? 256 : std::min(256, std::max(16, round16(2 * m)));
-  const int nt = (m + kLinMaxN - 1) / kLinMaxN;
-  return std::max(16, round16((m + nt - 1) / nt));
+template <typename TO, bool GATED, int MODE>
+static size_t lin_smem() {
+  const size_t smem = 1024 + kLinRing + sizeof(LinBars);
+  set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, (int)smem);
+  return smem;
+}
+
+// Clusters of `split` CTAs that run at the same time (a GPC's SMs are not a multiple of 8)
+static int lin_clusters(int split) {
+  static std::atomic<int> known[4];
+  const int i = split == 2 ? 0 : split == 4 ? 1 : 2;
+  int n = known[i].load(std::memory_order_relaxed);
+  if (n) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)split * 152);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) != cudaSuccess)
+    n = 0;
+  n = std::max(1, n);
+  known[i].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+struct LinPlan {
+  int mode, BN, split;
+  long tiles;
+};
+
+// How to cut the product: an estimate in SM cycles of the candidates, from the bytes that a CTA
+// loads for each k-block (about 48 a cycle), the MMA's time (2 cycles a column), and what a tile
+// or a cluster costs to start and to join.
+static LinPlan lin_plan(int R, int N, int E, int KB, bool gated) {
+  const int sms = dev_info().sms;
+  // experts that get rows, and rows of one of them, when rows fall on experts evenly
+  const double active = E > 1 ? E * (1.0 - std::pow(1.0 - 1.0 / E, R)) : 1.0;
+  const double m = R / active;
+  const int rows = gated ? 2 * N : N;
+  LinPlan best{};
+  double cost = 1e30;
+  for (int mode = 0; mode < 3; mode++)
+    for (int BN = 16; BN <= kLinMaxN; BN += 16)
+      for (int split = mode == kSplit ? 2 : 1; split <= (mode == kSplit ? 8 : 1); split *= 2) {
+        if (mode == kPair && (BN < 64 || BN % 32 || rows <= kLinM)) continue;
+        if (split > KB) continue;
+        const int FT = (rows + (mode == kPair ? 255 : 127)) / (mode == kPair ? 256 : 128);
+        // row tiles of an expert: exact when dense; by expert the last one is about half full,
+        // and experts differ in size
+        const double rt = E ? std::max(1.0, m / BN + 0.5) : (double)((R + BN - 1) / BN);
+        const double tiles = active * rt * FT;
+        const double width = mode == kPair    ? sms / 2
+                             : mode == kSplit ? lin_clusters(split)
+                                              : sms;
+        const double waves = E ? std::max(1.0, tiles / width + 0.3) : std::ceil(tiles / width);
+        const double cols = std::min((double)BN, m);
+        const double kb = std::max(2.0 * cols, (kLinM + (mode == kPair ? BN / 2 : BN)) * 128 / 48.0);
+        double c = waves * KB / split * kb + 1500;
+        if (mode == kSplit) {
+          if (tiles > width) continue;  // a cluster has one tile
+          c += 2500 + 8.0 * BN;
+        } else {
+          c += 4.0 * BN;  // the last tile's epilogue
+        }
+        if (c < cost * 0.999) {
+          cost = c;
+          best = LinPlan{mode, BN, split, 0};
+        }
+      }
+  const int FT = (rows + (best.mode == kPair ? 255 : 127)) / (best.mode == kPair ? 256 : 128);
+  // at most so many tiles exist, however the rows fall on the experts
+  const long rt = E ? (long)std::min(R, E) + R / best.BN : (R + best.BN - 1) / best.BN;
+  best.tiles = rt * FT;
+  return best;
+}
+
+template <typename TO, bool GATED, int MODE>
+static int launch_linear(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
+                         long tiles, cudaStream_t st) {
+  auto *k = linear_kernel<TO, GATED, MODE>;
+  const size_t smem = lin_smem<TO, GATED, MODE>();
+  const int per = MODE == kPair ? 2 : MODE == kSplit ? a.split : 1;  // CTAs per tile
+  const long most = MODE == kSplit ? tiles : std::min(tiles, (long)dev_info().sms / per);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most * per));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)per, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = MODE == kOne ? 1 : 2;
+  if (cudaLaunchKernelEx(&cfg, k, xm, wm, a) != cudaSuccess) return MOE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <typename TO, bool GATED>
-static int launch_linear(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
-                         cudaStream_t st) {
-  const size_t smem = 1024 + kLinRing + sizeof(LinBars);
-  set_dyn_smem((const void *)linear_kernel<TO, GATED>, (int)smem);
-  const long tiles = ((long)std::min(a.R, std::max(1, a.E)) + a.R / a.BN) * a.FT;
-  const int grid = (int)std::min((long)dev_info().sms, std::max(1l, tiles));
-  if (launch_pdl(linear_kernel<TO, GATED>, dim3(grid), dim3(kLinThreads), smem, st, xm, wm, a) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+static int launch_linear_m(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
+                           const LinPlan &p, cudaStream_t st) {
+  return p.mode == kPair    ? launch_linear<TO, GATED, kPair>(xm, wm, a, p.tiles, st)
+         : p.mode == kSplit ? launch_linear<TO, GATED, kSplit>(xm, wm, a, p.tiles, st)
+                            : launch_linear<TO, GATED, kOne>(xm, wm, a, p.tiles, st);
 }
 
 template <typename TO>
 static int launch_linear_t(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
-                           cudaStream_t st) {
-  return a.act == MOE_ACT_SWIGLU ? launch_linear<TO, true>(xm, wm, a, st)
-                                 : launch_linear<TO, false>(xm, wm, a, st);
+                           const LinPlan &p, cudaStream_t st) {
+  return a.act == MOE_ACT_SWIGLU ? launch_linear_m<TO, true>(xm, wm, a, p, st)
+                                 : launch_linear_m<TO, false>(xm, wm, a, p, st);
 }
 
 }  // namespace moe
@@ -460,9 +751,13 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   a.E = n_experts;
   a.ke = 128 / es;
   a.KB = (K + a.ke - 1) / a.ke;
-  a.BN = lin_bn(R, n_experts);
-  a.stages = std::min(kLinStages, kLinRing / ((kLinM + a.BN) * 128));
-  a.FT = gated ? (N + 63) / 64 : (N + kLinM - 1) / kLinM;
+  const LinPlan plan = lin_plan(R, N, n_experts, a.KB, gated);
+  const int xrows = plan.mode == kPair ? plan.BN / 2 : plan.BN;
+  const int ftw = (plan.mode == kPair ? 2 * kLinM : kLinM) / (gated ? 2 : 1);
+  a.BN = plan.BN;
+  a.split = plan.split;
+  a.stages = std::min(kLinStages, kLinRing / ((kLinM + xrows) * 128));
+  a.FT = (N + ftw - 1) / ftw;
   a.act = act;
   a.kind8 = es == 1;
   a.bf16 = dtype == MOE_DT_BF16;
@@ -474,7 +769,7 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   {
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)R};
     const cuuint64_t strides[1] = {(cuuint64_t)ldx * es};
-    const cuuint32_t box[2] = {(cuuint32_t)a.ke, (cuuint32_t)a.BN};
+    const cuuint32_t box[2] = {(cuuint32_t)a.ke, (cuuint32_t)xrows};
     if (enc(&xm, dt, 2, const_cast<void *>(x), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -499,7 +794,7 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   }
   if (cr != CUDA_SUCCESS) return MOE_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
-  return out_dtype == MOE_DT_F32    ? launch_linear_t<float>(xm, wm, a, st)
-         : out_dtype == MOE_DT_BF16 ? launch_linear_t<__nv_bfloat16>(xm, wm, a, st)
-                                    : launch_linear_t<__half>(xm, wm, a, st);
+  return out_dtype == MOE_DT_F32    ? launch_linear_t<float>(xm, wm, a, plan, st)
+         : out_dtype == MOE_DT_BF16 ? launch_linear_t<__nv_bfloat16>(xm, wm, a, plan, st)
+                                    : launch_linear_t<__half>(xm, wm, a, plan, st);
 }
