@@ -13,7 +13,7 @@
 //
 // A persistent CTA per SM walks the tiles of all experts.  Warp 0 issues TMA loads into a
 // ring of stages (128-byte swizzle; rows past an expert's weights, and the end of K, read as
-// zero), warp 1 issues tcgen05.mma into one of two accumulators in tensor memory, warps 2-5
+// zero), warp 1 issues tcgen05.mma into one of two accumulators in tensor memory, warps 2-9
 // turn the other accumulator into output.  For SwiGLU the weight map interleaves 16 gate
 // rows with their 16 up rows, so that a gate and its up value sit 16 lanes apart in one warp.
 #include <cuda.h>
@@ -35,8 +35,10 @@ constexpr int kLinM = 128;         // weight rows per CTA and tile
 constexpr int kLinMaxN = 256;      // token rows per tile
 constexpr int kLinStages = 12;     // ring slots at most
 constexpr int kLinMaxE = 256;
-constexpr int kLinThreads = 192;
-constexpr int kLinRing = 208 * 1024;  // shared memory of the ring
+constexpr int kLinEpi = 8;         // epilogue warps: two per quarter of the tensor-memory lanes
+constexpr int kLinThreads = 64 + 32 * kLinEpi;
+constexpr int kLinRing = 192 * 1024;  // shared memory of the ring
+constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk (32 features)
 constexpr long kLinWaitNs = 2000000000L;
 
 // How CTAs share a tile:
@@ -63,13 +65,15 @@ struct LinArgs {
   int split;         // kSplit: CTAs per tile
   int act;
   int kind8, bf16;   // operand type: e4m3, or bf16 / fp16
+  int vec;           // out's and residual's rows start on 16-byte boundaries
 };
 
 struct LinBars {
   uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort_flag;
-  alignas(16) float xs[4][kLinMaxN];  // token scales of the epilogue warps' tile
+  alignas(16) float xs[kLinEpi][kLinMaxN / 2];     // token scales of the epilogue warps' columns
+  alignas(16) float stage[kLinEpi][16 * kLinPitch];  // 16 columns of a warp on their way out
   int pre[kLinMaxE + 1];   // row tiles before each expert
   int off[kLinMaxE + 1];   // first row of each expert
 };
@@ -197,91 +201,115 @@ __device__ __forceinline__ LinTile lin_tile(const LinArgs &a, const LinBars *b, 
   return t;
 }
 
+// silu for an output of type TO: the fast form (relative error near 1e-6) where the result is
+// rounded to 16 bits, the library's exponential and division where it stays fp32
+template <typename TO>
+__device__ __forceinline__ float lin_silu(float z) {
+  return sizeof(TO) == 2 ? silu_fast(z) : silu_f(z);
+}
+
+template <typename TO>
 __device__ __forceinline__ float lin_act(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
-    case MOE_ACT_SILU: return silu_f(z);
+    case MOE_ACT_SILU: return lin_silu<TO>(z);
     case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
     default: return z;
   }
 }
 
-// What a lane of an epilogue warp needs to turn accumulator values of its weight row into
-// outputs: scales, bias, and where its columns go.
+// The epilogue of one warp: 32 weight rows (a lane each) of a tile.  Sixteen columns at a time
+// are scaled, biased and activated in registers, staged as fp32 in shared memory, and read back
+// so that a lane holds eight neighbouring features of one token: residual and output move as
+// 16-byte accesses.  (Two-byte stores straight from the registers, 64 bytes a column, took 25
+// instructions a column with their address arithmetic; the staged form takes about 7.)
 template <typename TO, bool GATED>
 struct LinOut {
-  float sw, bi;
-  const float *xs;   // token scales of the tile
-  TO *op;
+  static constexpr int F = GATED ? 16 : 32;              // output features of the warp
+  static constexpr int PITCH = GATED ? 16 : kLinPitch;   // floats per staged column
+  static constexpr int LPR = F / 8;                      // lanes that hold one token's features
+  static constexpr int RPI = 32 / LPR, IT = 16 / RPI;    // tokens per step, steps per chunk
+  float sw, bi;      // weight row's scale and bias
+  float *stage;
+  TO *op;            // this lane's features of the tile's first token
   const TO *rp;
   long ldout, ldres;
-  int cols;          // columns of the tile that this lane stores (0: its feature is past N)
+  int nf, vec;       // features that this lane stores (0..8); all 8, 16-byte aligned
   int up, act;       // of two columns, the lower lanes of a SwiGLU warp finish the first,
                      // the upper lanes the second
 
-  __device__ __forceinline__ LinOut(const LinArgs &a, const LinTile &t, int ft128, int row,
-                                    const float *xs_)
-      : xs(xs_), ldout(a.ldout), ldres(a.ldres), act(a.act) {
-    const int lane = row & 31;
-    int wr, f;  // this lane's weight row, and the output feature it (and its partner) give
+  __device__ __forceinline__ LinOut(const LinArgs &a, const LinTile &t, int ft128, int quad,
+                                    int lane, float *stage_)
+      : stage(stage_), ldout(a.ldout), ldres(a.ldres), act(a.act) {
     up = GATED && lane >= 16;
-    if (GATED) {
-      f = ft128 * 64 + (row >> 5) * 16 + (lane & 15);
-      wr = f + (up ? a.N : 0);
-    } else {
-      wr = f = ft128 * kLinM + row;
-    }
+    const int f0 = ft128 * (GATED ? 64 : kLinM) + quad * F;  // the warp's first feature
+    const int f = f0 + (GATED ? lane & 15 : lane);
     const bool in = f < a.N;
-    const long wi = (long)t.e * (GATED ? 2 * a.N : a.N) + wr;
+    const long wi = (long)t.e * (GATED ? 2 * a.N : a.N) + f + (up ? a.N : 0);
     sw = a.w_scale && in ? a.w_scale[wi] : 1.f;
     bi = a.bias && in ? a.bias[wi] : 0.f;
-    op = (TO *)a.out + (long)(t.r0 + up) * ldout + f;
-    rp = a.residual ? (const TO *)a.residual + (long)(t.r0 + up) * ldres + f : nullptr;
-    cols = in ? t.n - up : 0;
+    const int fo = f0 + 8 * (lane % LPR);
+    nf = min(max(a.N - fo, 0), 8);
+    vec = a.vec && nf == 8;
+    op = (TO *)a.out + (long)(t.r0 + lane / LPR) * ldout + fo;
+    rp = a.residual ? (const TO *)a.residual + (long)(t.r0 + lane / LPR) * ldres + fo : nullptr;
   }
 
-  static constexpr int S = GATED ? 2 : 1, J = 16 / S;
-
-  // the residual of columns c0 .. c0 + 15, loaded ahead of the accumulator's wait
-  __device__ __forceinline__ void prefetch(int c0, int end, float (&rv)[J]) const {
+  // the residual of columns c0 .. c0 + 15 (those below `end`), loaded ahead of the
+  // accumulator's wait
+  __device__ __forceinline__ void prefetch(int c0, int end, int lane, Pack<TO> (&rv)[IT]) const {
     if (!rp) return;
-    const int left = min(cols, end - up) - c0;
 #pragma unroll
-    for (int j = 0; j < J; j++)
-      rv[j] = S * j < left ? Elem<TO>::get(rp[(c0 + S * j) * ldres]) : 0.f;
+    for (int i = 0; i < IT; i++) {
+      if (c0 + i * RPI + lane / LPR >= end) continue;
+      const TO *r = rp + (long)(c0 + i * RPI) * ldres;
+      rv[i] = vec ? load_pack<TO, true>(r, 0, 8) : load_pack<TO, false>(r, 0, nf);
+    }
   }
 
-  // accumulator values v of columns c0 .. c0 + 15 (c0 a multiple of 4; columns at `end` and
-  // beyond are left out): scale, bias, activation, residual, store
-  __device__ __forceinline__ void finish(int c0, int end, const float (&v)[16],
-                                         const float (&rv)[J]) const {
-    float y[J];
+  // accumulator values v of columns c0 .. c0 + 15, whose token scales are xs[0 .. 15]; columns
+  // at `end` and beyond are left out
+  __device__ __forceinline__ void finish(int c0, int end, int lane, const float *xs,
+                                         const float (&v)[16], const Pack<TO> (&rv)[IT]) const {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-      const float4 s4 = *(const float4 *)(xs + c0 + j);
-      const float z0 = fmaf(v[j] * s4.x, sw, bi), z1 = fmaf(v[j + 1] * s4.y, sw, bi);
-      const float z2 = fmaf(v[j + 2] * s4.z, sw, bi), z3 = fmaf(v[j + 3] * s4.w, sw, bi);
+      const float4 s4 = *(const float4 *)(xs + j);
+      float z[4] = {fmaf(v[j] * s4.x, sw, bi), fmaf(v[j + 1] * s4.y, sw, bi),
+                    fmaf(v[j + 2] * s4.z, sw, bi), fmaf(v[j + 3] * s4.w, sw, bi)};
       if (GATED) {
-        const float o0 = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
-        const float o1 = __shfl_xor_sync(0xffffffffu, up ? z2 : z3, 16);
-        y[j / S] = up ? silu_f(o0) * z1 : silu_f(z0) * o0;
-        y[j / S + 1] = up ? silu_f(o1) * z3 : silu_f(z2) * o1;
+#pragma unroll
+        for (int p = 0; p < 4; p += 2) {
+          const float o = __shfl_xor_sync(0xffffffffu, up ? z[p] : z[p + 1], 16);
+          const float g = up ? o : z[p], u = up ? z[p + 1] : o;
+          stage[(j + p + up) * PITCH + (lane & 15)] = lin_silu<TO>(g) * u;
+        }
       } else {
-        y[j % J] = z0, y[(j + 1) % J] = z1, y[(j + 2) % J] = z2, y[(j + 3) % J] = z3;
+        if (act != MOE_ACT_NONE) {
+#pragma unroll
+          for (int p = 0; p < 4; p++) z[p] = lin_act<TO>(z[p], act);
+        }
+#pragma unroll
+        for (int p = 0; p < 4; p++) stage[(j + p) * PITCH + lane] = z[p];
       }
     }
-    if (!GATED && act != MOE_ACT_NONE) {
+    __syncwarp();
 #pragma unroll
-      for (int j = 0; j < J; j++) y[j] = lin_act(y[j], act);
+    for (int i = 0; i < IT; i++) {
+      const int c = i * RPI + lane / LPR;
+      if (c0 + c < end) {
+        float y[8];
+        *(float4 *)y = *(const float4 *)(stage + c * PITCH + 8 * (lane % LPR));
+        *(float4 *)(y + 4) = *(const float4 *)(stage + c * PITCH + 8 * (lane % LPR) + 4);
+        Pack<TO> o;
+#pragma unroll
+        for (int m = 0; m < 8; m++)
+          o.v[m] = Elem<TO>::put(rp ? y[m] + Elem<TO>::get(rv[i].v[m]) : y[m]);
+        TO *d = op + (long)(c0 + i * RPI) * ldout;
+        if (vec) store_pack<TO, true>(d, 0, 8, o);
+        else store_pack<TO, false>(d, 0, nf, o);
+      }
     }
-    if (rp) {
-#pragma unroll
-      for (int j = 0; j < J; j++) y[j] += rv[j];
-    }
-    const int left = min(cols, end - up) - c0;
-#pragma unroll
-    for (int j = 0; j < J; j++)
-      if (S * j < left) op[(c0 + S * j) * ldout] = Elem<TO>::put(y[j]);
+    __syncwarp();
   }
 };
 
@@ -304,7 +332,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&b->acc_full[i], 1);
-      tc::mbar_init(&b->acc_empty[i], PAIR ? 8 : 4);
+      tc::mbar_init(&b->acc_empty[i], PAIR ? 2 * kLinEpi : kLinEpi);
     }
     tc::mbar_init(&b->drain, 1);
     b->abort_flag = 0;
@@ -461,41 +489,44 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else if (!SPLIT) {
     // -------------------------------------------------- epilogue: a lane per weight row
-    const int quad = warp & 3;  // the warp's quarter of the tensor-memory lanes
-    float *xs = b->xs[quad];
+    const int quad = warp & 3;         // the warp's quarter of the tensor-memory lanes
+    const int half = (warp - 2) >> 2;  // of its chunks of 16 columns, the even or the odd ones
+    float *xs = b->xs[warp - 2];
     int buf = 0;
     uint32_t bph = 0;
     for (int tile = cta; tile < total; tile += ctas) {
       const LinTile t = lin_tile(a, b, tile);
-      // the tile's token scales, a copy per warp (1 where there are none, 0 past the rows)
+      // the token scales of the warp's columns (1 where there are none, 0 past the rows)
+      for (int i = lane; i < kLinMaxN / 2; i += 32) {
+        const int c = 32 * (i >> 4) + 16 * half + (i & 15);
+        xs[i] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
+      }
       __syncwarp();
-      for (int c = lane; c < a.BN; c += 32)
-        xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
-      __syncwarp();
-      const LinOut<TO, GATED> o(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad * 32 + lane, xs);
+      const LinOut<TO, GATED> o(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad, lane,
+                                b->stage[warp - 2]);
       if (!__all_sync(0xffffffffu,
                       tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
         break;
       tc::fence_after_sync();
       const uint32_t taddr = tbase + buf * kLinMaxN + ((uint32_t)(32 * quad) << 16);
-      for (int c0 = 0; c0 < t.n; c0 += 16) {
+      for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
         uint32_t v[16];
-        float f[16], rv[LinOut<TO, GATED>::J];
+        float f[16];
+        Pack<TO> rv[LinOut<TO, GATED>::IT];
         __syncwarp();
         tc::tmem_ld16(taddr + c0, v);
-        o.prefetch(c0, t.n, rv);
+        o.prefetch(c0, t.n, lane, rv);
         tc::tmem_wait_ld();
-        if (c0 + 16 >= t.n) {  // the accumulator is read: the next tile may use it
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR) arrive_in_cta(&b->acc_empty[buf], 0);
-            else tc::mbar_arrive(&b->acc_empty[buf]);
-          }
-        }
 #pragma unroll
         for (int j = 0; j < 16; j++) f[j] = __uint_as_float(v[j]);
-        o.finish(c0, t.n, f, rv);
+        o.finish(c0, t.n, lane, xs + (c0 >> 1) - 8 * half, f, rv);
+      }
+      // the accumulator is read: the next tile may use it
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) arrive_in_cta(&b->acc_empty[buf], 0);
+        else tc::mbar_arrive(&b->acc_empty[buf]);
       }
       if (buf) bph ^= 1;
       buf ^= 1;
@@ -505,15 +536,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------- a tile's partial sums, joined
     // A cluster has at most one tile.  Column c belongs to CTA c / cpc; once every CTA's MMAs
     // are done its ring holds the partial sums [from CTA][own column][weight row].
-    const int quad = warp & 3, row = quad * 32 + lane;
+    const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
     const bool work = cta < total;
     const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
-    float *xs = b->xs[quad];
+    float *xs = b->xs[0];  // of all columns
     bool ok = work;
     LinTile t{};
     if (work) t = lin_tile(a, b, cta);
     if (warp >= 2 && work) {
-      for (int c = lane; c < a.BN; c += 32)
+      for (int c = tid - 64; c < kLinMaxN; c += 32 * kLinEpi)
         xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
       ok = __all_sync(0xffffffffu, tc::mbar_wait_backoff(&b->acc_full[0], 0, abort, kLinWaitNs, 32));
       tc::fence_after_sync();
@@ -522,7 +553,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     cluster_sync();
     if (warp >= 2 && ok) {
       const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16);
-      for (int c0 = 0; c0 < t.n; c0 += 16) {
+      for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
         uint32_t v[16];
         __syncwarp();
         tc::tmem_ld16(taddr + c0, v);
@@ -539,27 +570,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncwarp();
     cluster_sync();
     if (warp >= 2 && ok) {
-      const LinOut<TO, GATED> o(a, t, t.ft, row, xs);
+      const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, b->stage[warp - 2]);
       const float *part = (const float *)ring;
       const int c1 = min(t.n, (int)(rank + 1) * cpc);
-      for (int c0 = rank * cpc; c0 < c1; c0 += 16) {
-        float f[16], rv[LinOut<TO, GATED>::J];
-        o.prefetch(c0, c1, rv);
+      for (int c0 = rank * cpc + 16 * half; c0 < c1; c0 += 32) {
+        float f[16];
+        Pack<TO> rv[LinOut<TO, GATED>::IT];
+        o.prefetch(c0, c1, lane, rv);
 #pragma unroll
         for (int j = 0; j < 16; j++) f[j] = 0.f;
         for (int q = 0; q < a.split; q++)
 #pragma unroll
           for (int j = 0; j < 16; j++)
             if (c0 + j < c1) f[j] += part[(q * cpc + c0 + j - (int)rank * cpc) * kLinM + row];
-        o.finish(c0, c1, f, rv);
+        o.finish(c0, c1, lane, xs + c0, f, rv);
       }
     }
   }
   // rows of no expert are zero
   if (a.E && warp >= 2) {
     const long tail = b->off[a.E], lead = b->off[0];
-    const long first = (long)blockIdx.x * 128 + (warp - 2) * 32 + lane;
-    const long step = (long)gridDim.x * 128;
+    const long first = (long)blockIdx.x * 32 * kLinEpi + tid - 64;
+    const long step = (long)gridDim.x * 32 * kLinEpi;
     TO *out = (TO *)a.out;
     for (long i = first; i < lead * a.N; i += step)
       out[i / a.N * a.ldout + i % a.N] = Elem<TO>::put(0.f);
@@ -761,6 +793,8 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   a.act = act;
   a.kind8 = es == 1;
   a.bf16 = dtype == MOE_DT_BF16;
+  a.vec = ((uintptr_t)out | (uintptr_t)residual | (uintptr_t)(ldout * eo) |
+           (uintptr_t)(residual ? ldres * eo : 0)) % 16 == 0;
 
   const CUtensorMapDataType dt = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                          : CU_TENSOR_MAP_DATA_TYPE_UINT16;
