@@ -32,7 +32,6 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, -1, -2,
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_NUMERIC, MOE_ERR_PACKED = -4, -5, -6, -7
 MOE_ROUTER_SOFTMAX, MOE_ROUTER_SIGMOID_GROUPED = 0, 1
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16, MOE_DT_E4M3 = 0, 1, 2, 3
-ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 # every entry point include/moe.h declares
 EXPORTED = [
@@ -46,6 +45,9 @@ EXPORTED = [
     "moe_sort_tokens", "moe_dispatch_rows", "moe_dispatch_rows_grad", "moe_combine_rows",
     "moe_combine_rows_grad", "moe_linear",
 ]
+_TOKEN_OPERATORS = ("moe_rmsnorm_e4m3", "moe_sort_tokens", "moe_dispatch_rows",
+                    "moe_dispatch_rows_grad", "moe_combine_rows", "moe_combine_rows_grad",
+                    "moe_linear", "ACTIVATIONS")
 
 # stages bracketed by the events of moe_layer_forward_timed
 STAGES = ["router", "permute", "act_encode", "gate_up", "down", "combine"]
@@ -319,189 +321,11 @@ def moe_quantize_rows(w, bits, q, scale, stream=None):
                                 _stream(stream)), "moe_quantize_rows")
 
 
-# ----------------------------------------------------------------------- token operators
-_DTYPES = None  # torch dtype -> moe_dtype, filled on first use (torch is imported late)
-
-
-def _row_type(t) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16,
-                   torch.float16: MOE_DT_F16, torch.float8_e4m3fn: MOE_DT_E4M3}
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"rows must be float32, bfloat16, float16 or float8_e4m3fn, "
-                        f"got {t.dtype}") from None
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rows(t, shape, name, like=None, dtype=None):
-    """Check a [rows, n] operand (rows may be strided); returns its row distance."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same(t, name, like, dtype)
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
-
-
-def _flat(t, shape, name, like=None, dtype=None):
-    """Check a contiguous operand."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same(t, name, like, dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _same(t, name, like, dtype):
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-
-
-def moe_rmsnorm_e4m3(x, q, scale, add=None, weight=None, resid=None, eps=1e-6, group=0,
-                     normalize=True, stream=None):
-    """r = x + add -> resid; q (float8_e4m3fn [T, H]) and scale (fp32 [T, ceil(H / group)],
-    group 0: one a row) of r * weight / sqrt(mean(r^2) + eps).  normalize=False quantises
-    r * weight itself."""
-    import torch
-    T, H = x.shape
-    dt = x.dtype
-    ldx = _rows(x, x.shape, "x")
-    ldq = _rows(q, x.shape, "q", x, torch.float8_e4m3fn)
-    groups = -(-H // group) if group > 0 else 1
-    _flat(scale, (T, groups), "scale", x, torch.float32)
-    ldadd = _rows(add, x.shape, "add", x, dt) if add is not None else 0
-    ldr = _rows(resid, x.shape, "resid", x, dt) if resid is not None else 0
-    if weight is not None:
-        _flat(weight, (H,), "weight", x, dt)
-    _ck(lib().moe_rmsnorm_e4m3(T, H, x.data_ptr(), ldx, _row_type(x), _ptr(add), ldadd,
-                               _ptr(weight), eps, int(normalize), group, _ptr(resid), ldr,
-                               q.data_ptr(), ldq, scale.data_ptr(), _stream(stream)),
-        "moe_rmsnorm_e4m3")
-
-
-def moe_sort_tokens(ids, n_experts, offsets, perm, slot_pos, stream=None):
-    """ids int32 [T, k] -> offsets [E + 1], perm [T * k], slot_pos [T, k], all int32."""
-    import torch
-    T, k = ids.shape
-    i32 = torch.int32
-    _flat(ids, ids.shape, "ids", None, i32)
-    _flat(offsets, (n_experts + 1,), "offsets", ids, i32)
-    _flat(perm, (T * k,), "perm", ids, i32)
-    _flat(slot_pos, ids.shape, "slot_pos", ids, i32)
-    _ck(lib().moe_sort_tokens(T, k, int(n_experts), ids.data_ptr(), offsets.data_ptr(),
-                              perm.data_ptr(), slot_pos.data_ptr(), _stream(stream)),
-        "moe_sort_tokens")
-
-
-def moe_dispatch_rows(x, slot_pos, offsets, xs, scale=None, scale_s=None, stream=None):
-    """xs[slot_pos[t, j]] = x[t] ([T * k, H], the rest zero); scale [T, S] -> scale_s alike."""
-    import torch
-    (T, H), k = x.shape, slot_pos.shape[1]
-    ldx = _rows(x, x.shape, "x")
-    _flat(xs, (T * k, H), "xs", x, x.dtype)
-    _flat(slot_pos, (T, k), "slot_pos", x, torch.int32)
-    _flat(offsets, offsets.shape, "offsets", x, torch.int32)
-    S = ldsc = 0
-    if scale is not None:
-        S = scale.shape[1]
-        ldsc = _rows(scale, (T, S), "scale", x, torch.float32)
-        _flat(scale_s, (T * k, S), "scale_s", x, torch.float32)
-    _ck(lib().moe_dispatch_rows(T, k, offsets.numel() - 1, H, _row_type(x), x.data_ptr(), ldx,
-                                slot_pos.data_ptr(), offsets.data_ptr(), xs.data_ptr(), S,
-                                _ptr(scale), ldsc, _ptr(scale_s), _stream(stream)),
-        "moe_dispatch_rows")
-
-
-def moe_combine_rows(y, slot_pos, out, w=None, add=None, stream=None):
-    """out[t] = add[t] + sum_j w[t, j] * y[slot_pos[t, j]] (slots of -1 left out)."""
-    import torch
-    T, k = slot_pos.shape
-    H = out.shape[1]
-    _flat(y, (T * k, H), "y")
-    _flat(slot_pos, slot_pos.shape, "slot_pos", y, torch.int32)
-    ldo = _rows(out, (T, H), "out", y)
-    lda = _rows(add, (T, H), "add", y, out.dtype) if add is not None else 0
-    if w is not None:
-        _flat(w, (T, k), "w", y, torch.float32)
-    _ck(lib().moe_combine_rows(T, k, H, y.data_ptr(), _row_type(y), slot_pos.data_ptr(), _ptr(w),
-                               _ptr(add), lda, out.data_ptr(), ldo, _row_type(out),
-                               _stream(stream)), "moe_combine_rows")
-
-
-def moe_combine_rows_grad(dout, y, slot_pos, offsets, w, dy, dw, stream=None):
-    """dy[slot_pos[t, j]] = w[t, j] * dout[t] (the rest zero), dw[t, j] = <dout[t], y[slot]>."""
-    import torch
-    (T, k), H = slot_pos.shape, dout.shape[1]
-    ldd = _rows(dout, (T, H), "dout")
-    _flat(y, (T * k, H), "y", dout, dout.dtype)
-    _flat(dy, (T * k, H), "dy", dout, dout.dtype)
-    _flat(dw, (T, k), "dw", dout, torch.float32)
-    _flat(slot_pos, (T, k), "slot_pos", dout, torch.int32)
-    _flat(offsets, offsets.shape, "offsets", dout, torch.int32)
-    if w is not None:
-        _flat(w, (T, k), "w", dout, torch.float32)
-    _ck(lib().moe_combine_rows_grad(T, k, offsets.numel() - 1, H, _row_type(dout),
-                                    dout.data_ptr(), ldd, y.data_ptr(), slot_pos.data_ptr(),
-                                    offsets.data_ptr(), _ptr(w), dy.data_ptr(), dw.data_ptr(),
-                                    _stream(stream)), "moe_combine_rows_grad")
-
-
-def moe_dispatch_rows_grad(dxs, slot_pos, dx, stream=None):
-    """dx[t] = sum_j dxs[slot_pos[t, j]] (slots of -1 left out)."""
-    import torch
-    T, k = slot_pos.shape
-    H = dx.shape[1]
-    _flat(dxs, (T * k, H), "dxs")
-    _flat(slot_pos, slot_pos.shape, "slot_pos", dxs, torch.int32)
-    ldx = _rows(dx, (T, H), "dx", dxs)
-    _ck(lib().moe_dispatch_rows_grad(T, k, H, _row_type(dxs), dxs.data_ptr(),
-                                     slot_pos.data_ptr(), dx.data_ptr(), ldx, _row_type(dx),
-                                     _stream(stream)), "moe_dispatch_rows_grad")
-
-
-def moe_linear(x, w, out, x_scale=None, w_scale=None, bias=None, act="none", residual=None,
-               offsets=None, status=None, stream=None):
-    """out = act((x w^T) * x_scale * w_scale + bias) + residual; see ACTIVATIONS for act.
-
-    Dense: w [N, K] (SwiGLU: [2N, K], gate rows first).  By expert: w [E, N, K] and offsets
-    int32 [E + 1], rows offsets[e] .. offsets[e + 1] of x using expert e; w_scale and bias
-    have w's leading dimensions."""
-    import torch
-    (R, K), N = x.shape, out.shape[1]
-    if act not in ACTIVATIONS:
-        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
-    E = 0 if offsets is None else offsets.numel() - 1
-    rows = 2 * N if act == "swiglu" else N
-    lead = (rows,) if offsets is None else (E, rows)
-    f32 = torch.float32
-    if offsets is not None:
-        if E < 1:
-            raise ValueError("offsets must hold E + 1 values")
-        _flat(offsets, (E + 1,), "offsets", x, torch.int32)
-    ldx = _rows(x, (R, K), "x")
-    _flat(w, lead + (K,), "w", x, x.dtype)
-    ldo = _rows(out, (R, N), "out", x)
-    ldr = _rows(residual, (R, N), "residual", x, out.dtype) if residual is not None else 0
-    if x_scale is not None:
-        if x_scale.dim() == 2:
-            x_scale = x_scale[:, 0] if x_scale.shape[1] == 1 else x_scale
-        _flat(x_scale, (R,), "x_scale", x, f32)
-    if w_scale is not None:
-        _flat(w_scale, lead, "w_scale", x, f32)
-    if bias is not None:
-        _flat(bias, lead, "bias", x, f32)
-    if status is not None:
-        _flat(status, (1,), "status", x, torch.int32)
-    _ck(lib().moe_linear(R, N, K, E, x.data_ptr(), ldx, _row_type(x), _ptr(x_scale),
-                         w.data_ptr(), _ptr(w_scale), _ptr(bias), ACTIVATIONS[act],
-                         _ptr(residual), ldr, _ptr(offsets), out.data_ptr(), ldo,
-                         _row_type(out), _ptr(status), _stream(stream)), "moe_linear")
+def __getattr__(name):
+    """The token operators live in tokens.py, which imports torch; they load on first use."""
+    if name in _TOKEN_OPERATORS:
+        from . import tokens
+        for n in _TOKEN_OPERATORS:
+            globals()[n] = getattr(tokens, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

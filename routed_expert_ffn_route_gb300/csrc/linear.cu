@@ -37,7 +37,7 @@ constexpr int kLinStages = 12;     // ring slots at most
 constexpr int kLinMaxE = 256;
 constexpr int kLinEpi = 8;         // epilogue warps: two per quarter of the tensor-memory lanes
 constexpr int kLinThreads = 64 + 32 * kLinEpi;
-constexpr int kLinRing = 192 * 1024;  // shared memory of the ring
+constexpr int kLinRing = 192 * 1024;  // shared memory of the ring and the exchange, at most
 constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk (32 features)
 constexpr long kLinWaitNs = 2000000000L;
 
@@ -63,6 +63,9 @@ struct LinArgs {
   int BN, stages;    // token rows per tile, ring slots
   int FT;            // feature tiles (of 128 weight rows, kPair: 256)
   int split;         // kSplit: CTAs per tile
+  int ring;          // bytes of the ring
+  int exchange;      // kSplit: bytes of the partial sums' exchange behind it
+  int tmem;          // tensor-memory columns
   int act;
   int kind8, bf16;   // operand type: e4m3, or bf16 / fp16
   int vec;           // out's and residual's rows start on 16-byte boundaries
@@ -84,9 +87,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ void prefetch_map(const void *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // the address of a shared-memory object in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
@@ -104,22 +116,29 @@ __device__ __forceinline__ void store_in_cta(uint32_t addr, float v) {
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void lin_tmem_alloc(uint32_t *dst) {  // whole warp, all 512 columns
+__device__ __forceinline__ void lin_tmem_alloc(uint32_t *dst, uint32_t columns) {  // whole warp
   if (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     tc::smem_u32(dst))
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32(dst)),
+                 "r"(columns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   } else {
-    tc::tmem_alloc<512>(dst);
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32(dst)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 }
 template <bool PAIR>
-__device__ __forceinline__ void lin_tmem_free(uint32_t t) {
+__device__ __forceinline__ void lin_tmem_free(uint32_t t, uint32_t columns) {
   if (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(columns)
+                 : "memory");
   else
-    tc::tmem_dealloc<512>(t);
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(columns)
+                 : "memory");
 }
 
 // one MMA: 32 bytes of K (32 e4m3 or 16 16-bit elements); PAIR: over both CTAs' tiles
@@ -322,9 +341,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint8_t *ring = tc::align_smem_1024(smraw);
   const int xrows = PAIR ? a.BN / 2 : a.BN;  // token rows in this CTA's stages
   const int stage_bytes = (kLinM + xrows) * 128;
-  LinBars *b = (LinBars *)(ring + kLinRing);
+  LinBars *b = (LinBars *)(ring + a.ring + a.exchange);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = MODE == kOne ? 0 : cluster_rank();
+  if (SPLIT) cluster_arrive();  // waited for before the first store into another CTA
+  if (tid == 32) {
+    prefetch_map(&xmap);
+    prefetch_map(&wmap);
+  }
   if (tid == 0) {
     for (int s = 0; s < a.stages; s++) {
       tc::mbar_init(&b->full[s], 1);
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncwarp();
   // tensor memory before the trigger: a successor may start as soon as every CTA has
   // triggered, and must not take columns that this grid still has to allocate
-  if (warp == 0) lin_tmem_alloc<PAIR>(&b->tmem);
+  if (warp == 0) lin_tmem_alloc<PAIR>(&b->tmem, a.tmem);
   pdl_wait();
   pdl_trigger();
   // the experts' rows, clamped to [0, R] and kept in order, so that no offset leads out of x
@@ -378,7 +402,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   }
   tc::fence_before_sync();
-  if (MODE == kOne) __syncthreads(); else cluster_sync();  // barriers are ready in every CTA
+  if (PAIR) cluster_sync(); else __syncthreads();  // PAIR: barriers are ready in both CTAs
   tc::fence_after_sync();
   const uint32_t tbase = b->tmem;
   volatile int *abort = &b->abort_flag;
@@ -534,8 +558,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   if (SPLIT) {
     // ---------------------------------------------------- a tile's partial sums, joined
-    // A cluster has at most one tile.  Column c belongs to CTA c / cpc; once every CTA's MMAs
-    // are done its ring holds the partial sums [from CTA][own column][weight row].
+    // A cluster has at most one tile.  Column c belongs to CTA c / cpc, whose exchange area
+    // receives the partial sums [from CTA][own column][weight row].
     const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
     const bool work = cta < total;
     const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
@@ -543,6 +567,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     bool ok = work;
     LinTile t{};
     if (work) t = lin_tile(a, b, cta);
+    const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, b->stage[(warp - 2) & (kLinEpi - 1)]);
     if (warp >= 2 && work) {
       for (int c = tid - 64; c < kLinMaxN; c += 32 * kLinEpi)
         xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
@@ -550,7 +575,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc::fence_after_sync();
     }
     __syncwarp();
-    cluster_sync();
+    cluster_wait();  // every CTA of the cluster has started: its memory may be written
     if (warp >= 2 && ok) {
       const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16);
       for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
@@ -562,7 +587,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int j = 0; j < 16; j++) {
           const int to = (c0 + j) / cpc, c = c0 + j - to * cpc;
           if (c0 + j < t.n)
-            store_in_cta(in_cta(ring, to) + (uint32_t)(((rank * cpc + c) * kLinM + row) * 4),
+            store_in_cta(in_cta(ring + a.ring, to) + (uint32_t)(((rank * cpc + c) * kLinM + row) * 4),
                          __uint_as_float(v[j]));
         }
       }
@@ -570,8 +595,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncwarp();
     cluster_sync();
     if (warp >= 2 && ok) {
-      const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, b->stage[warp - 2]);
-      const float *part = (const float *)ring;
+      const float *part = (const float *)(ring + a.ring);
       const int c1 = min(t.n, (int)(rank + 1) * cpc);
       for (int c0 = rank * cpc + 16 * half; c0 < c1; c0 += 32) {
         float f[16];
@@ -600,9 +624,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   __syncwarp();
   tc::fence_before_sync();
-  if (MODE == kOne) __syncthreads(); else cluster_sync();  // nobody still uses a peer's memory
+  if (PAIR) cluster_sync(); else __syncthreads();  // nobody still uses a peer's barriers
   tc::fence_after_sync();
-  if (warp == 0) lin_tmem_free<PAIR>(tbase);
+  if (warp == 0) lin_tmem_free<PAIR>(tbase, a.tmem);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
@@ -618,10 +642,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
 }
 
 template <typename TO, bool GATED, int MODE>
-static size_t lin_smem() {
-  const size_t smem = 1024 + kLinRing + sizeof(LinBars);
-  set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, (int)smem);
-  return smem;
+static size_t lin_smem(int bytes) {  // of the ring and the exchange
+  set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, 1024 + kLinRing + (int)sizeof(LinBars));
+  return 1024 + bytes + sizeof(LinBars);
 }
 
 // Clusters of `split` CTAs that run at the same time (a GPC's SMs are not a multiple of 8)
@@ -633,7 +656,7 @@ static int lin_clusters(int split) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)split * 152);
   cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>();
+  cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>(kLinRing);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)split, 1, 1};
@@ -654,7 +677,7 @@ struct LinPlan {
 // How to cut the product: an estimate in SM cycles of the candidates, from the bytes that a CTA
 // loads for each k-block (about 48 a cycle), the MMA's time (2 cycles a column), and what a tile
 // or a cluster costs to start and to join.
-static LinPlan lin_plan(int R, int N, int E, int KB, bool gated) {
+static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
   const int sms = dev_info().sms;
   // experts that get rows, and rows of one of them, when rows fall on experts evenly
   const double active = E > 1 ? E * (1.0 - std::pow(1.0 - 1.0 / E, R)) : 1.0;
@@ -697,11 +720,29 @@ static LinPlan lin_plan(int R, int N, int E, int KB, bool gated) {
   return best;
 }
 
+// the plans of the last sizes seen by this thread (the estimate costs about a launch)
+static LinPlan lin_plan(int R, int N, int E, int KB, bool gated) {
+  struct Entry {
+    int R, N, E, KB, gated, dev;
+    LinPlan plan;
+  };
+  static thread_local Entry seen[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint32_t h = ((uint32_t)R * 2654435761u) ^ ((uint32_t)N * 2246822519u) ^
+                     ((uint32_t)KB * 3266489917u) ^ (uint32_t)(E * 2 + gated) * 668265263u;
+  Entry &e = seen[(h >> 16) & 63];
+  if (e.R == R && e.N == N && e.E == E && e.KB == KB && e.gated == gated && e.dev == dev)
+    return e.plan;
+  e = Entry{R, N, E, KB, gated, dev, lin_make_plan(R, N, E, KB, gated)};
+  return e.plan;
+}
+
 template <typename TO, bool GATED, int MODE>
 static int launch_linear(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
                          long tiles, cudaStream_t st) {
   auto *k = linear_kernel<TO, GATED, MODE>;
-  const size_t smem = lin_smem<TO, GATED, MODE>();
+  const size_t smem = lin_smem<TO, GATED, MODE>(a.ring + a.exchange);
   const int per = MODE == kPair ? 2 : MODE == kSplit ? a.split : 1;  // CTAs per tile
   const long most = MODE == kSplit ? tiles : std::min(tiles, (long)dev_info().sms / per);
   cudaLaunchConfig_t cfg = {};
@@ -788,7 +829,20 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   const int ftw = (plan.mode == kPair ? 2 * kLinM : kLinM) / (gated ? 2 : 1);
   a.BN = plan.BN;
   a.split = plan.split;
-  a.stages = std::min(kLinStages, kLinRing / ((kLinM + xrows) * 128));
+  const int stage = (kLinM + xrows) * 128;
+  a.stages = std::min(kLinStages, kLinRing / stage);
+  a.tmem = 512;
+  if (plan.mode == kSplit) {
+    // one tile a CTA: no more stages than its part of K has k-blocks, and, where that leaves
+    // four, little enough memory that the next launch's CTA fits beside it on the SM
+    const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
+    a.exchange = a.split * cpc * kLinM * 4;
+    const int half = (110 * 1024 - (int)sizeof(LinBars) - 1024 - a.exchange) / stage;
+    const int most = std::min(kLinStages, (kLinRing - a.exchange) / stage);
+    a.stages = std::min((a.KB + a.split - 1) / a.split, half >= 4 ? std::min(half, most) : most);
+    for (a.tmem = 32; a.tmem < a.BN; a.tmem *= 2) {}
+  }
+  a.ring = a.stages * stage;
   a.FT = (N + ftw - 1) / ftw;
   a.act = act;
   a.kind8 = es == 1;

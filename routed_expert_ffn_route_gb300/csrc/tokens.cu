@@ -44,9 +44,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
   const unsigned below = (1u << lane) - 1u;
   pdl_wait();
   pdl_trigger();
-  const int runs = ncta * kSortWarps;
+  const int nw = blockDim.x >> 5;
+  const int runs = ncta * nw;
   const int len = ((n + runs - 1) / runs + 31) / 32 * 32;  // slots per warp
-  const long lo = min((long)n, (long)(rank * kSortWarps + warp) * len);
+  const long lo = min((long)n, (long)(rank * nw + warp) * len);
   const long hi = min((long)n, lo + len);
   for (int e = lane; e < E; e += 32) hist[warp][e] = 0;
   __syncwarp();
@@ -62,14 +63,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
   __syncthreads();
   for (int e = tid; e < E; e += blockDim.x) {  // exclusive scan over the warps
     int s = 0;
-    for (int w = 0; w < kSortWarps; w++) {
+    for (int w = 0; w < nw; w++) {
       const int c = hist[w][e];
       hist[w][e] = s;
       s += c;
     }
     total[e] = s;
   }
-  cl.sync();
+  if (ncta > 1) cl.sync(); else __syncthreads();
   for (int e = tid; e < E; e += blockDim.x) {
     int before = 0, all = 0;
     for (int c = 0; c < ncta; c++) {
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
       all += v;
     }
     start[e] = all;
-    for (int w = 0; w < kSortWarps; w++) hist[w][e] += before;
+    for (int w = 0; w < nw; w++) hist[w][e] += before;
   }
   __syncthreads();
   if (warp == 0) {  // exclusive scan over the experts
@@ -119,11 +120,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
     if (pos >= 0) perm[pos] = (int32_t)i;
   }
   // dropped slots leave a tail without rows
-  for (long p = (long)start[E] + rank * kSortThreads + tid; p < n; p += (long)ncta * kSortThreads)
+  for (long p = (long)start[E] + rank * blockDim.x + tid; p < n; p += (long)ncta * blockDim.x)
     perm[p] = -1;
   if (rank == 0)
     for (int e = tid; e <= E; e += blockDim.x) offsets[e] = start[e];
-  cl.sync();  // no CTA leaves while another may still read its totals
+  if (ncta > 1) cl.sync();  // no CTA leaves while another may still read its totals
 }
 
 // ----------------------------------------------------------------------- row movement
@@ -189,46 +190,51 @@ struct CombineArgs {
   const float *w;
   void *out;
   long ldadd, ldout;
-  int T, k, H, packs;
+  int T, k, H;
 };
 
-// A thread per pack of eight elements of a token's row: k loads in flight (eight at a time),
-// fp32 sum in slot order, one rounding.
-template <typename TY, typename TO, bool VEC>
+// A thread per pack of eight elements of a token's row: the rows of U slots are in flight at a
+// time; fp32 sum in slot order, one rounding.
+template <typename TY, typename TO, bool VEC, int U>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const CombineArgs a) {
-  constexpr int U = 8;
   pdl_wait();
   pdl_trigger();
-  const long item = (long)blockIdx.x * kRowThreads + threadIdx.x;
-  const long t = item / a.packs;
-  if (t >= a.T) return;
-  const int i = 8 * (int)(item - t * a.packs);
-  const long n = (long)a.T * a.k;
+  const int t = blockIdx.y * blockDim.y + threadIdx.y;
+  const int i = 8 * (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  if (t >= a.T || i >= a.H) return;
+  const int n = a.T * a.k;
   const TY *y = (const TY *)a.y;
+  const int32_t *slots = a.slot_pos + (long)t * a.k;
+  const float *ws = a.w ? a.w + (long)t * a.k : nullptr;
   float acc[8];
-  if (a.add) {
-    const Pack<TO> p = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
+  Pack<TO> pa;
+  if (a.add) pa = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
 #pragma unroll
-    for (int m = 0; m < 8; m++) acc[m] = Elem<TO>::get(p.v[m]);
-  } else {
-#pragma unroll
-    for (int m = 0; m < 8; m++) acc[m] = 0.f;
-  }
+  for (int m = 0; m < 8; m++) acc[m] = 0.f;
+  bool first = true;
   for (int j0 = 0; j0 < a.k; j0 += U) {
     int pos[U];
+    float w[U];
     Pack<TY> v[U];
 #pragma unroll
     for (int j = 0; j < U; j++) {
-      pos[j] = j0 + j < a.k ? a.slot_pos[t * a.k + j0 + j] : -1;
+      pos[j] = j0 + j < a.k ? slots[j0 + j] : -1;
       if (pos[j] >= n) pos[j] = -1;
-      if (pos[j] >= 0) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
+      w[j] = ws && j0 + j < a.k ? ws[j0 + j] : 1.0f;
     }
+#pragma unroll
+    for (int j = 0; j < U; j++)
+      if (pos[j] >= 0) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
+    if (first && a.add) {  // the addend is waited for after the rows are on their way
+#pragma unroll
+      for (int m = 0; m < 8; m++) acc[m] = Elem<TO>::get(pa.v[m]);
+    }
+    first = false;
 #pragma unroll
     for (int j = 0; j < U; j++) {
       if (pos[j] < 0) continue;
-      const float w = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
 #pragma unroll
-      for (int m = 0; m < 8; m++) acc[m] = fmaf(w, Elem<TY>::get(v[j].v[m]), acc[m]);
+      for (int m = 0; m < 8; m++) acc[m] = fmaf(w[j], Elem<TY>::get(v[j].v[m]), acc[m]);
     }
   }
   Pack<TO> o;
@@ -318,16 +324,24 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
   }
 }
 
+template <typename TY, typename TO, bool VEC>
+static cudaError_t launch_combine_v(const CombineArgs &a, cudaStream_t st) {
+  const int packs = (a.H + 7) / 8;
+  int bx = 32;  // short rows: several tokens a CTA
+  while (bx < packs && bx < kRowThreads) bx *= 2;
+  const dim3 block(bx, kRowThreads / bx);
+  const dim3 grid((packs + bx - 1) / bx, (a.T + block.y - 1) / block.y);
+  if (a.k <= 2) return launch_pdl(combine_rows_kernel<TY, TO, VEC, 2>, grid, block, 0, st, a);
+  if (a.k <= 4) return launch_pdl(combine_rows_kernel<TY, TO, VEC, 4>, grid, block, 0, st, a);
+  return launch_pdl(combine_rows_kernel<TY, TO, VEC, 8>, grid, block, 0, st, a);
+}
+
 template <typename TY, typename TO>
-static cudaError_t launch_combine_rows(const CombineArgs &a0, cudaStream_t st) {
-  CombineArgs a = a0;
-  a.packs = (a.H + 7) / 8;
+static cudaError_t launch_combine_rows(const CombineArgs &a, cudaStream_t st) {
   const uintptr_t p = (uintptr_t)a.y | (uintptr_t)a.add | (uintptr_t)a.out |
                       (uintptr_t)(a.ldadd * sizeof(TO)) | (uintptr_t)(a.ldout * sizeof(TO));
-  const bool vec = p % 16 == 0 && a.H % 8 == 0;
-  const dim3 grid((unsigned)(((long)a.T * a.packs + kRowThreads - 1) / kRowThreads));
-  return vec ? launch_pdl(combine_rows_kernel<TY, TO, true>, grid, dim3(kRowThreads), 0, st, a)
-             : launch_pdl(combine_rows_kernel<TY, TO, false>, grid, dim3(kRowThreads), 0, st, a);
+  return p % 16 == 0 && a.H % 8 == 0 ? launch_combine_v<TY, TO, true>(a, st)
+                                     : launch_combine_v<TY, TO, false>(a, st);
 }
 
 template <typename T, bool VEC>
@@ -396,7 +410,9 @@ int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *of
   const int ctas = n <= kSortThreads * 2 ? 1 : kSortCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
+  // one CTA: a warp for every 32 slots, and the scans' threads; fewer warps, shorter scans
+  cfg.blockDim = dim3(ctas > 1 ? kSortThreads
+                               : std::min(kSortThreads, std::max(256, (n + 31) / 32 * 32)));
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -458,7 +474,7 @@ int moe_combine_rows(int T, int k, int H, const void *y, moe_dtype y_dtype,
   if ((uintptr_t)y % ey || ((uintptr_t)out | (uintptr_t)add) % eo ||
       ((uintptr_t)slot_pos | (uintptr_t)w) % 4)
     return MOE_ERR_INVALID_ARG;
-  const CombineArgs a{y, add, slot_pos, w, out, add ? ldadd : 0, ldout, T, k, H, 0};
+  const CombineArgs a{y, add, slot_pos, w, out, add ? ldadd : 0, ldout, T, k, H};
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
   if (y_dtype == MOE_DT_F32)
