@@ -39,6 +39,7 @@ constexpr int kLinEpi = 8;         // epilogue warps: two per quarter of the ten
 constexpr int kLinThreads = 64 + 32 * kLinEpi;
 constexpr int kLinRing = 192 * 1024;  // shared memory of the ring and the exchange, at most
 constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk (32 features)
+constexpr int kLinStage = kLinEpi * 16 * kLinPitch * 4;  // bytes of the staged chunks
 constexpr long kLinWaitNs = 2000000000L;
 
 // How CTAs share a tile:
@@ -65,18 +66,16 @@ struct LinArgs {
   int split;         // kSplit: CTAs per tile
   int ring;          // bytes of the ring
   int exchange;      // kSplit: bytes of the partial sums' exchange behind it
-  int tmem;          // tensor-memory columns
   int act;
   int kind8, bf16;   // operand type: e4m3, or bf16 / fp16
   int vec;           // out's and residual's rows start on 16-byte boundaries
 };
 
-struct LinBars {
+struct alignas(16) LinBars {
   uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort_flag;
   alignas(16) float xs[kLinEpi][kLinMaxN / 2];     // token scales of the epilogue warps' columns
-  alignas(16) float stage[kLinEpi][16 * kLinPitch];  // 16 columns of a warp on their way out
   int pre[kLinMaxE + 1];   // row tiles before each expert
   int off[kLinMaxE + 1];   // first row of each expert
 };
@@ -111,34 +110,31 @@ __device__ __forceinline__ void arrive_in_cta(uint64_t *bar, uint32_t rank) {
                    in_cta(bar, rank))
                : "memory");
 }
-__device__ __forceinline__ void store_in_cta(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void store_in_cta(uint32_t addr, const uint32_t *v) {  // 16 bytes
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void lin_tmem_alloc(uint32_t *dst, uint32_t columns) {  // whole warp
-  if (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     tc::smem_u32(dst)),
-                 "r"(columns)
+// Tensor memory of a CTA: two accumulators of 256 columns; kSplit has one, and its number is a
+// constant of the instruction, without which the driver gives such a kernel whole SMs.
+template <int MODE>
+__device__ __forceinline__ void lin_tmem_alloc(uint32_t *dst) {  // whole warp
+  if (MODE == kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     tc::smem_u32(dst))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     tc::smem_u32(dst)),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc::tmem_alloc<MODE == kSplit ? kLinMaxN : 2 * kLinMaxN>(dst);
   }
 }
-template <bool PAIR>
-__device__ __forceinline__ void lin_tmem_free(uint32_t t, uint32_t columns) {
-  if (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(columns)
-                 : "memory");
+template <int MODE>
+__device__ __forceinline__ void lin_tmem_free(uint32_t t) {
+  if (MODE == kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
   else
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(columns)
-                 : "memory");
+    tc::tmem_dealloc<MODE == kSplit ? kLinMaxN : 2 * kLinMaxN>(t);
 }
 
 // one MMA: 32 bytes of K (32 e4m3 or 16 16-bit elements); PAIR: over both CTAs' tiles
@@ -333,7 +329,9 @@ struct LinOut {
 };
 
 template <typename TO, bool GATED, int MODE>
-__global__ void __launch_bounds__(kLinThreads, 1)
+// (registers are given out to whole sets of four warps: 12 warps' worth a CTA, so that two
+// kSplit CTAs share an SM only with the registers of 384 threads each)
+__global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kSplit ? 2 : 1)
     linear_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                   const LinArgs a) {
   constexpr bool PAIR = MODE == kPair, SPLIT = MODE == kSplit;
@@ -343,6 +341,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int stage_bytes = (kLinM + xrows) * 128;
   LinBars *b = (LinBars *)(ring + a.ring + a.exchange);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // 16 columns of each epilogue warp on their way out: behind the barriers, kSplit: in the
+  // ring, which is idle by then
+  float *stage = (float *)(SPLIT ? ring : (uint8_t *)(b + 1)) +
+                 ((warp - 2) & (kLinEpi - 1)) * (16 * kLinPitch);
   const uint32_t rank = MODE == kOne ? 0 : cluster_rank();
   if (SPLIT) cluster_arrive();  // waited for before the first store into another CTA
   if (tid == 32) {
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncwarp();
   // tensor memory before the trigger: a successor may start as soon as every CTA has
   // triggered, and must not take columns that this grid still has to allocate
-  if (warp == 0) lin_tmem_alloc<PAIR>(&b->tmem, a.tmem);
+  if (warp == 0) lin_tmem_alloc<MODE>(&b->tmem);
   pdl_wait();
   pdl_trigger();
   // the experts' rows, clamped to [0, R] and kept in order, so that no offset leads out of x
@@ -526,8 +528,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         xs[i] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
       }
       __syncwarp();
-      const LinOut<TO, GATED> o(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad, lane,
-                                b->stage[warp - 2]);
+      const LinOut<TO, GATED> o(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad, lane, stage);
       if (!__all_sync(0xffffffffu,
                       tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
         break;
@@ -559,15 +560,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (SPLIT) {
     // ---------------------------------------------------- a tile's partial sums, joined
     // A cluster has at most one tile.  Column c belongs to CTA c / cpc, whose exchange area
-    // receives the partial sums [from CTA][own column][weight row].
+    // receives the partial sums [from CTA][four own columns][weight row][4]: a lane sends four
+    // columns of its row in one store (a store a column, and a division to find its owner, took
+    // 14 us where this takes 3: 200 columns between four CTAs).
     const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
     const bool work = cta < total;
     const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
+    const uint32_t inv = 65536u / cpc + 1;  // exact for columns below 256
     float *xs = b->xs[0];  // of all columns
     bool ok = work;
     LinTile t{};
     if (work) t = lin_tile(a, b, cta);
-    const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, b->stage[(warp - 2) & (kLinEpi - 1)]);
+    const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, stage);
     if (warp >= 2 && work) {
       for (int c = tid - 64; c < kLinMaxN; c += 32 * kLinEpi)
         xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
@@ -584,18 +588,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tc::tmem_ld16(taddr + c0, v);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-          const int to = (c0 + j) / cpc, c = c0 + j - to * cpc;
+        for (int j = 0; j < 16; j += 4) {
+          const uint32_t to = ((uint32_t)(c0 + j) * inv) >> 16;  // (c0 + j) / cpc
           if (c0 + j < t.n)
-            store_in_cta(in_cta(ring + a.ring, to) + (uint32_t)(((rank * cpc + c) * kLinM + row) * 4),
-                         __uint_as_float(v[j]));
+            store_in_cta(in_cta(ring + a.ring, to) +
+                             (rank * cpc + c0 + j - to * cpc) * (kLinM * 4) + row * 16,
+                         v + j);
         }
       }
     }
     __syncwarp();
     cluster_sync();
     if (warp >= 2 && ok) {
-      const float *part = (const float *)(ring + a.ring);
+      const uint8_t *part = ring + a.ring + row * 16;
       const int c1 = min(t.n, (int)(rank + 1) * cpc);
       for (int c0 = rank * cpc + 16 * half; c0 < c1; c0 += 32) {
         float f[16];
@@ -605,8 +610,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int j = 0; j < 16; j++) f[j] = 0.f;
         for (int q = 0; q < a.split; q++)
 #pragma unroll
-          for (int j = 0; j < 16; j++)
-            if (c0 + j < c1) f[j] += part[(q * cpc + c0 + j - (int)rank * cpc) * kLinM + row];
+          for (int j = 0; j < 16; j += 4) {
+            if (c0 + j >= c1) continue;
+            const float4 p =
+                *(const float4 *)(part + (q * cpc + c0 + j - (int)rank * cpc) * (kLinM * 4));
+            f[j] += p.x, f[j + 1] += p.y, f[j + 2] += p.z, f[j + 3] += p.w;
+          }
         o.finish(c0, c1, lane, xs + c0, f, rv);
       }
     }
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tc::fence_before_sync();
   if (PAIR) cluster_sync(); else __syncthreads();  // nobody still uses a peer's barriers
   tc::fence_after_sync();
-  if (warp == 0) lin_tmem_free<PAIR>(tbase, a.tmem);
+  if (warp == 0) lin_tmem_free<MODE>(tbase);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
@@ -643,18 +652,41 @@ static PFN_cuTensorMapEncodeTiled_v12000 lin_encode() {
 
 template <typename TO, bool GATED, int MODE>
 static size_t lin_smem(int bytes) {  // of the ring and the exchange
-  set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, 1024 + kLinRing + (int)sizeof(LinBars));
-  return 1024 + bytes + sizeof(LinBars);
+  const int more = 1024 + (int)sizeof(LinBars) + (MODE == kSplit ? 0 : kLinStage);
+  set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, kLinRing + more);
+  return bytes + more;
 }
 
-// Clusters of `split` CTAs that run at the same time (a GPC's SMs are not a multiple of 8)
+// Shared memory of a kSplit CTA.  It has one tile, so no more stages than its part of K has
+// k-blocks; and, where that leaves four, little enough that two CTAs fit on an SM: clusters of
+// eight otherwise leave SMs of a GPC idle (15 run at a time), and the next launch's CTAs can
+// start beside this one's.
+struct LinSplit {
+  int stages, ring, exchange;
+  bool two;  // two CTAs fit on an SM
+};
+static LinSplit lin_split(int BN, int split, int KB) {
+  const int stage = (kLinM + BN) * 128;
+  const int cpc = ((BN + split - 1) / split + 3) & ~3;
+  LinSplit r;
+  r.exchange = split * cpc * kLinM * 4;
+  const int room = 112 * 1024 - (int)sizeof(LinBars) - 1024 - r.exchange;
+  const int most = std::min({kLinStages, (kLinRing - r.exchange) / stage, (KB + split - 1) / split});
+  const int small = std::min(most, room / stage);
+  r.two = room >= kLinStage && small >= std::min(most, 4);
+  r.stages = r.two ? small : most;
+  r.ring = std::max(r.stages * stage, kLinStage);  // the output is staged there
+  return r;
+}
+
+// Clusters of `split` CTAs that run at the same time with one CTA on an SM
 static int lin_clusters(int split) {
-  static std::atomic<int> known[4];
-  const int i = split == 2 ? 0 : split == 4 ? 1 : 2;
-  int n = known[i].load(std::memory_order_relaxed);
+  static std::atomic<int> known[3];
+  std::atomic<int> &k = known[split == 2 ? 0 : split == 4 ? 1 : 2];
+  int n = k.load(std::memory_order_relaxed);
   if (n) return n;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)split * 152);
+  cfg.gridDim = dim3((unsigned)split * dev_info().sms);
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>(kLinRing);
   cudaLaunchAttribute attr[1];
@@ -665,7 +697,7 @@ static int lin_clusters(int split) {
   if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) != cudaSuccess)
     n = 0;
   n = std::max(1, n);
-  known[i].store(n, std::memory_order_relaxed);
+  k.store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -674,9 +706,12 @@ struct LinPlan {
   long tiles;
 };
 
-// How to cut the product: an estimate in SM cycles of the candidates, from the bytes that a CTA
-// loads for each k-block (about 48 a cycle), the MMA's time (2 cycles a column), and what a tile
-// or a cluster costs to start and to join.
+// How to cut the product: an estimate in SM cycles of each candidate, from what was measured.
+// A k-block takes as long as its MMAs (2 cycles a column: the tensor cores' rate for 256 columns
+// of 128 rows), its loads (2.45 cycles a 128-byte row, 52 bytes a cycle into an SM) or 430
+// cycles, whichever is longest; joining a split tile takes 2000 cycles and 12 a column and
+// other CTA.  One token of 6144 x 2048 bf16: split 8 6.8 us, 4 9.4, 2 15.0, none 24.9; 200
+// tokens of 4096 x 4096: 112 columns split 2 13.4 us, 208 split 4 15.0, 64 unsplit 18.8.
 static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
   const int sms = dev_info().sms;
   // experts that get rows, and rows of one of them, when rows fall on experts evenly
@@ -695,18 +730,19 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
         // and experts differ in size
         const double rt = E ? std::max(1.0, m / BN + 0.5) : (double)((R + BN - 1) / BN);
         const double tiles = active * rt * FT;
-        const double width = mode == kPair    ? sms / 2
-                             : mode == kSplit ? lin_clusters(split)
-                                              : sms;
-        const double waves = E ? std::max(1.0, tiles / width + 0.3) : std::ceil(tiles / width);
         const double cols = std::min((double)BN, m);
-        const double kb = std::max(2.0 * cols, (kLinM + (mode == kPair ? BN / 2 : BN)) * 128 / 48.0);
-        double c = waves * KB / split * kb + 1500;
-        if (mode == kSplit) {
-          if (tiles > width) continue;  // a cluster has one tile
-          c += 2500 + 8.0 * BN;
+        const double kb = std::max({2.0 * cols, 430.0,
+                                    2.45 * (kLinM + (mode == kPair ? BN / 2 : BN))});
+        double c;
+        if (mode == kSplit) {  // one tile a cluster
+          const LinSplit sp = lin_split(BN, split, KB);
+          if (sp.stages < 2 || tiles > lin_clusters(split) * (sp.two ? 2 : 1)) continue;
+          const double shared = tiles * split > sms ? 1.25 : 1.0;  // some SMs have two CTAs
+          c = (KB + split - 1) / split * kb * shared + 2000 + 12.0 * BN * (split - 1);
         } else {
-          c += 4.0 * BN;  // the last tile's epilogue
+          const double width = mode == kPair ? sms / 2 : sms;
+          const double waves = E ? std::max(1.0, tiles / width + 0.3) : std::ceil(tiles / width);
+          c = waves * KB * kb + 500 + 4.0 * BN;  // the last tile's epilogue
         }
         if (c < cost * 0.999) {
           cost = c;
@@ -831,18 +867,13 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   a.split = plan.split;
   const int stage = (kLinM + xrows) * 128;
   a.stages = std::min(kLinStages, kLinRing / stage);
-  a.tmem = 512;
-  if (plan.mode == kSplit) {
-    // one tile a CTA: no more stages than its part of K has k-blocks, and, where that leaves
-    // four, little enough memory that the next launch's CTA fits beside it on the SM
-    const int cpc = ((a.BN + a.split - 1) / a.split + 3) & ~3;
-    a.exchange = a.split * cpc * kLinM * 4;
-    const int half = (110 * 1024 - (int)sizeof(LinBars) - 1024 - a.exchange) / stage;
-    const int most = std::min(kLinStages, (kLinRing - a.exchange) / stage);
-    a.stages = std::min((a.KB + a.split - 1) / a.split, half >= 4 ? std::min(half, most) : most);
-    for (a.tmem = 32; a.tmem < a.BN; a.tmem *= 2) {}
-  }
   a.ring = a.stages * stage;
+  if (plan.mode == kSplit) {
+    const LinSplit sp = lin_split(a.BN, a.split, a.KB);
+    a.stages = sp.stages;
+    a.ring = sp.ring;
+    a.exchange = sp.exchange;
+  }
   a.FT = (N + ftw - 1) / ftw;
   a.act = act;
   a.kind8 = es == 1;
