@@ -312,13 +312,17 @@ struct LinOut {
     for (int i = 0; i < IT; i++) {
       const int c = i * RPI + lane / LPR;
       if (c0 + c < end) {
-        float y[8];
+        alignas(16) float y[8];
         *(float4 *)y = *(const float4 *)(stage + c * PITCH + 8 * (lane % LPR));
         *(float4 *)(y + 4) = *(const float4 *)(stage + c * PITCH + 8 * (lane % LPR) + 4);
-        Pack<TO> o;
+        if (rp) {
+          float r[8];
+          rv[i].get(r);
 #pragma unroll
-        for (int m = 0; m < 8; m++)
-          o.v[m] = Elem<TO>::put(rp ? y[m] + Elem<TO>::get(rv[i].v[m]) : y[m]);
+          for (int m = 0; m < 8; m++) y[m] += r[m];
+        }
+        Pack<TO> o;
+        o.put(y);
         TO *d = op + (long)(c0 + i * RPI) * ldout;
         if (vec) store_pack<TO, true>(d, 0, 8, o);
         else store_pack<TO, false>(d, 0, nf, o);

@@ -193,54 +193,66 @@ struct CombineArgs {
   int T, k, H;
 };
 
-// A thread per pack of eight elements of a token's row: the rows of U slots are in flight at a
-// time; fp32 sum in slot order, one rounding.
-template <typename TY, typename TO, bool VEC, int U>
+// A thread computes P packs of eight elements of a token's row, with U slots' rows (and the
+// addend) in flight for each; fp32 sum in slot order, one rounding.
+template <typename TY, typename TO, bool VEC, int U, int P>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const CombineArgs a) {
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.y * blockDim.y + threadIdx.y;
-  const int i = 8 * (int)(blockIdx.x * blockDim.x + threadIdx.x);
-  if (t >= a.T || i >= a.H) return;
+  const int i0 = 8 * (int)(blockIdx.x * blockDim.x * P + threadIdx.x), step = 8 * blockDim.x;
+  if (t >= a.T || i0 >= a.H) return;
   const int n = a.T * a.k;
   const TY *y = (const TY *)a.y;
   const int32_t *slots = a.slot_pos + (long)t * a.k;
   const float *ws = a.w ? a.w + (long)t * a.k : nullptr;
-  float acc[8];
-  Pack<TO> pa;
-  if (a.add) pa = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
+  const TO *add = a.add ? (const TO *)a.add + t * a.ldadd : nullptr;
+  Pack<TO> pa[P];
+  float acc[P][8];
 #pragma unroll
-  for (int m = 0; m < 8; m++) acc[m] = 0.f;
-  bool first = true;
+  for (int p = 0; p < P; p++) {
+    pa[p].clear();
+    if (add && i0 + p * step < a.H) pa[p] = load_pack<TO, VEC>(add, i0 + p * step, a.H);
+  }
   for (int j0 = 0; j0 < a.k; j0 += U) {
     int pos[U];
     float w[U];
-    Pack<TY> v[U];
+    Pack<TY> v[P][U];
 #pragma unroll
     for (int j = 0; j < U; j++) {
       pos[j] = j0 + j < a.k ? slots[j0 + j] : -1;
       if (pos[j] >= n) pos[j] = -1;
-      w[j] = ws && j0 + j < a.k ? ws[j0 + j] : 1.0f;
+      w[j] = pos[j] < 0 ? 0.f : ws ? ws[j0 + j] : 1.0f;  // a slot without a row adds zero
     }
 #pragma unroll
-    for (int j = 0; j < U; j++)
-      if (pos[j] >= 0) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
-    if (first && a.add) {  // the addend is waited for after the rows are on their way
+    for (int p = 0; p < P; p++)
 #pragma unroll
-      for (int m = 0; m < 8; m++) acc[m] = Elem<TO>::get(pa.v[m]);
+      for (int j = 0; j < U; j++) {
+        v[p][j].clear();
+        if (pos[j] >= 0 && i0 + p * step < a.H)
+          v[p][j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i0 + p * step, a.H);
+      }
+    if (j0 == 0) {  // the addend is waited for after the rows are on their way
+#pragma unroll
+      for (int p = 0; p < P; p++) pa[p].get(acc[p]);
     }
-    first = false;
 #pragma unroll
-    for (int j = 0; j < U; j++) {
-      if (pos[j] < 0) continue;
+    for (int p = 0; p < P; p++)
 #pragma unroll
-      for (int m = 0; m < 8; m++) acc[m] = fmaf(w[j], Elem<TY>::get(v[j].v[m]), acc[m]);
-    }
+      for (int j = 0; j < U; j++) {
+        float f[8];
+        v[p][j].get(f);
+#pragma unroll
+        for (int m = 0; m < 8; m++) acc[p][m] = fmaf(w[j], f[m], acc[p][m]);
+      }
   }
-  Pack<TO> o;
 #pragma unroll
-  for (int m = 0; m < 8; m++) o.v[m] = Elem<TO>::put(acc[m]);
-  store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i, a.H, o);
+  for (int p = 0; p < P; p++) {
+    if (i0 + p * step >= a.H) continue;
+    Pack<TO> o;
+    o.put(acc[p]);
+    store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i0 + p * step, a.H, o);
+  }
 }
 
 struct GradArgs {
@@ -267,8 +279,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
   if ((int)blockIdx.x >= a.T) {
     const long live = min(n, (long)max(0, a.offsets[a.E]));
     Pack<T> zero;
-#pragma unroll
-    for (int m = 0; m < 8; m++) zero.v[m] = Elem<T>::put(0.f);
+    zero.clear();
     for (long p = live + (blockIdx.x - a.T); p < n; p += gridDim.x - a.T)
       for (int i = 8 * tid; i < a.H; i += 8 * blockDim.x)
         store_pack<T, VEC>(dy + p * a.H, i, a.H, zero);
@@ -292,20 +303,24 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
       const Pack<T> pd = load_pack<T, VEC>(dout, i, a.H);
       Pack<T> py[KC];
 #pragma unroll
-      for (int j = 0; j < KC; j++)
+      for (int j = 0; j < KC; j++) {
+        py[j].clear();
         if (pos[j] >= 0) py[j] = load_pack<T, VEC>(y + (long)pos[j] * a.H, i, a.H);
+      }
       float d[8];
-#pragma unroll
-      for (int m = 0; m < 8; m++) d[m] = Elem<T>::get(pd.v[m]);
+      pd.get(d);
 #pragma unroll
       for (int j = 0; j < KC; j++) {
         if (pos[j] < 0) continue;
-        Pack<T> o;
+        float f[8], g[8];
+        py[j].get(f);
 #pragma unroll
         for (int m = 0; m < 8; m++) {
-          acc[j] = fmaf(d[m], Elem<T>::get(py[j].v[m]), acc[j]);
-          o.v[m] = Elem<T>::put(w[j] * d[m]);
+          acc[j] = fmaf(d[m], f[m], acc[j]);
+          g[m] = w[j] * d[m];
         }
+        Pack<T> o;
+        o.put(g);
         store_pack<T, VEC>(dy + (long)pos[j] * a.H, i, a.H, o);
       }
     }
@@ -324,16 +339,27 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
   }
 }
 
+template <typename TY, typename TO, bool VEC, int U, int P>
+static cudaError_t launch_combine_up(const CombineArgs &a, cudaStream_t st) {
+  const int packs = (a.H + 7) / 8, per = (packs + P - 1) / P;
+  int bx = 32;  // short rows: several tokens a CTA
+  while (bx < per && bx < kRowThreads) bx *= 2;
+  const dim3 block(bx, kRowThreads / bx);
+  const dim3 grid((per + bx - 1) / bx, (a.T + block.y - 1) / block.y);
+  return launch_pdl(combine_rows_kernel<TY, TO, VEC, U, P>, grid, block, 0, st, a);
+}
+
 template <typename TY, typename TO, bool VEC>
 static cudaError_t launch_combine_v(const CombineArgs &a, cudaStream_t st) {
-  const int packs = (a.H + 7) / 8;
-  int bx = 32;  // short rows: several tokens a CTA
-  while (bx < packs && bx < kRowThreads) bx *= 2;
-  const dim3 block(bx, kRowThreads / bx);
-  const dim3 grid((packs + bx - 1) / bx, (a.T + block.y - 1) / block.y);
-  if (a.k <= 2) return launch_pdl(combine_rows_kernel<TY, TO, VEC, 2>, grid, block, 0, st, a);
-  if (a.k <= 4) return launch_pdl(combine_rows_kernel<TY, TO, VEC, 4>, grid, block, 0, st, a);
-  return launch_pdl(combine_rows_kernel<TY, TO, VEC, 8>, grid, block, 0, st, a);
+  // enough rows to fill the GPU: more packs a thread where few slots are in flight
+  const bool many = (long)a.T * a.H >= (long)dev_info().sms * 2048 * 8 * 4;
+  if (a.k <= 2)
+    return many ? launch_combine_up<TY, TO, VEC, 2, 4>(a, st)
+                : launch_combine_up<TY, TO, VEC, 2, 1>(a, st);
+  if (a.k <= 4)
+    return many ? launch_combine_up<TY, TO, VEC, 4, 2>(a, st)
+                : launch_combine_up<TY, TO, VEC, 4, 1>(a, st);
+  return launch_combine_up<TY, TO, VEC, 8, 1>(a, st);
 }
 
 template <typename TY, typename TO>
