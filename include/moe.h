@@ -319,7 +319,7 @@ int moe_rmsnorm_e4m3(int T, int H, const void *x, long ldx, moe_dtype dtype, con
  * offsets [E+1]: first row of each expert (offsets[E] = rows in all); perm [T*k]: slot
  * t*k+j of each row; slot_pos [T][k]: row of each slot.  Ids outside [0, E) are dropped:
  * slot_pos -1, and perm ends in as many -1.  The order is stable, ids of one token may
- * repeat.  k <= 16, E <= 256, T <= 65535 (these operators: else MOE_ERR_UNSUPPORTED). */
+ * repeat.  k <= 16, E <= 256, T <= 65535, and for the rows below H <= 2^24 (else MOE_ERR_UNSUPPORTED). */
 int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *offsets,
                     int32_t *perm, int32_t *slot_pos, void *stream);
 

@@ -624,16 +624,18 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
       }
     }
   }
-  // rows of no expert are zero
+  // rows of no expert are zero: those before the first expert's and after the last one's
   if (a.E && warp >= 2) {
-    const long tail = b->off[a.E], lead = b->off[0];
-    const long first = (long)blockIdx.x * 32 * kLinEpi + tid - 64;
-    const long step = (long)gridDim.x * 32 * kLinEpi;
-    TO *out = (TO *)a.out;
-    for (long i = first; i < lead * a.N; i += step)
-      out[i / a.N * a.ldout + i % a.N] = Elem<TO>::put(0.f);
-    for (long i = first; i < (a.R - tail) * a.N; i += step)
-      out[(tail + i / a.N) * a.ldout + i % a.N] = Elem<TO>::put(0.f);
+    const int lead = b->off[0], rest = lead + a.R - b->off[a.E];
+    Pack<TO> zero;
+    zero.clear();
+    for (int i = blockIdx.x; i < rest; i += gridDim.x) {
+      TO *row = (TO *)a.out + (long)(i < lead ? i : b->off[a.E] + i - lead) * a.ldout;
+      for (int f = 8 * (tid - 64); f < a.N; f += 8 * 32 * kLinEpi) {
+        if (a.vec && f + 8 <= a.N) store_pack<TO, true>(row, f, a.N, zero);
+        else store_pack<TO, false>(row, f, a.N, zero);
+      }
+    }
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -658,7 +660,9 @@ template <typename TO, bool GATED, int MODE>
 static size_t lin_smem(int bytes) {  // of the ring and the exchange
   const int more = 1024 + (int)sizeof(LinBars) + (MODE == kSplit ? 0 : kLinStage);
   set_dyn_smem((const void *)linear_kernel<TO, GATED, MODE>, kLinRing + more);
-  return bytes + more;
+  // kSplit: never a third CTA on an SM.  Two hold all of its tensor memory; a third would wait
+  // for columns while its cluster's other CTAs hold those that the first two wait for elsewhere.
+  return std::max(bytes + more, MODE == kSplit ? 80 * 1024 : 0);
 }
 
 // Shared memory of a kSplit CTA.  It has one tile, so no more stages than its part of K has
