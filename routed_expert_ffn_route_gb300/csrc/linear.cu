@@ -63,6 +63,7 @@ struct LinArgs {
   int KB, ke;        // k-blocks, elements per k-block
   int BN, stages;    // token rows per tile, ring slots
   int FT;            // feature tiles (of 128 weight rows, kPair: 256)
+  int group;         // row tiles taken together
   int split;         // kSplit: CTAs per tile
   int ring;          // bytes of the ring
   int exchange;      // kSplit: bytes of the partial sums' exchange behind it
@@ -194,8 +195,10 @@ __device__ __forceinline__ void lin_load_5d(void *dst, const void *map, uint32_t
 }
 #undef LIN_TMA
 
-// A tile: rows [r0, r0 + n) of expert e, feature tile ft.  Row tiles run fastest, so that
-// CTAs working at the same time share weight tiles in L2.
+// A tile: rows [r0, r0 + n) of expert e, feature tile ft.  Tiles run over `group` row tiles, then
+// over the features, then over the groups: the CTAs working at one time then cover about as many
+// token rows as weight rows, and both stay in L2 (32768 x 6144 tokens, larger than L2, by 4096
+// features e4m3: 608 us with all row tiles first).
 struct LinTile {
   int e, ft, r0, n;
 };
@@ -208,10 +211,12 @@ __device__ __forceinline__ LinTile lin_tile(const LinArgs &a, const LinBars *b, 
   }
   const int rt_n = b->pre[lo + 1] - b->pre[lo];
   const int i = tile - b->pre[lo] * a.FT;
+  const int g = i / (a.group * a.FT);
+  const int gn = min(a.group, rt_n - g * a.group), j = i - g * a.group * a.FT;
   LinTile t;
   t.e = lo;
-  t.ft = i / rt_n;
-  t.r0 = b->off[lo] + (i - t.ft * rt_n) * a.BN;
+  t.ft = j / gn;
+  t.r0 = b->off[lo] + (g * a.group + j - t.ft * gn) * a.BN;
   t.n = min(a.BN, b->off[lo + 1] - t.r0);
   return t;
 }
@@ -883,6 +888,9 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
     a.exchange = sp.exchange;
   }
   a.FT = (N + ftw - 1) / ftw;
+  // as many token rows as weight rows at one time, when every SM works on a tile
+  const double at_once = plan.mode == kPair ? dev_info().sms / 2 : dev_info().sms;
+  a.group = std::max(1, (int)std::lround(std::sqrt(at_once * ftw * (gated ? 2 : 1) / a.BN)));
   a.act = act;
   a.kind8 = es == 1;
   a.bf16 = dtype == MOE_DT_BF16;
