@@ -232,65 +232,61 @@ struct CombineArgs {
   int T, k, H;
 };
 
-// A thread computes P packs of eight elements of a token's row, with U slots' rows (and the
-// addend) in flight for each; fp32 sum in slot order, one rounding.
-template <typename TY, typename TO, bool VEC, int U, int P>
+// A thread owns a pack of eight elements of the rows of tokens t, t + stride, ...: U slots' rows
+// (and the addend) in flight at a time, the next token's slots loaded meanwhile, so that only
+// the first token waits for slots before its rows; fp32 sum in slot order, one rounding.
+// 8192 tokens x 8 of 6144 bf16: 151 us, 6.7 TB/s (a CTA per token and eight slots in flight:
+// 184; four 169); x 2 of 4096: 49 us, 5.5 TB/s (two to four tokens or packs a thread: 48 to 61).
+template <typename TY, typename TO, bool VEC, int U>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const CombineArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.y * blockDim.y + threadIdx.y;
-  const int i0 = 8 * (int)(blockIdx.x * blockDim.x * P + threadIdx.x), step = 8 * blockDim.x;
-  if (t >= a.T || i0 >= a.H) return;
+  const int i = 8 * (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  const int stride = gridDim.y * blockDim.y;
+  int t = blockIdx.y * blockDim.y + threadIdx.y;
+  if (t >= a.T || i >= a.H) return;
   const int n = a.T * a.k;
   const TY *y = (const TY *)a.y;
-  const int32_t *slots = a.slot_pos + (long)t * a.k;
-  const float *ws = a.w ? a.w + (long)t * a.k : nullptr;
-  const TO *add = a.add ? (const TO *)a.add + t * a.ldadd : nullptr;
-  Pack<TO> pa[P];
-  float acc[P][8];
-#pragma unroll
-  for (int p = 0; p < P; p++) {
-    pa[p].clear();
-    if (add && i0 + p * step < a.H) pa[p] = load_pack<TO, VEC>(add, i0 + p * step, a.H);
-  }
-  for (int j0 = 0; j0 < a.k; j0 += U) {
-    int pos[U];
-    float w[U];
-    Pack<TY> v[P][U];
+  int pos[U];
+  float w[U];
+  auto slots = [&](int token, int j0) {
 #pragma unroll
     for (int j = 0; j < U; j++) {
-      pos[j] = j0 + j < a.k ? slots[j0 + j] : -1;
-      if (pos[j] >= n) pos[j] = -1;
-      w[j] = pos[j] < 0 ? 0.f : ws ? ws[j0 + j] : 1.0f;  // a slot without a row adds zero
+      const bool in = token < a.T && j0 + j < a.k;
+      const long s = (long)token * a.k + j0 + j;
+      pos[j] = in ? a.slot_pos[s] : -1;
+      w[j] = in ? a.w ? a.w[s] : 1.0f : 0.f;
     }
-#pragma unroll
-    for (int p = 0; p < P; p++)
+  };
+  slots(t, 0);
+  for (; t < a.T; t += stride) {
+    Pack<TO> pa;
+    pa.clear();
+    if (a.add) pa = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
+    float acc[8];
+    for (int j0 = 0; j0 < a.k; j0 += U) {
+      Pack<TY> v[U];
+      float wv[U];
 #pragma unroll
       for (int j = 0; j < U; j++) {
-        v[p][j].clear();
-        if (pos[j] >= 0 && i0 + p * step < a.H)
-          v[p][j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i0 + p * step, a.H);
+        const bool live = pos[j] >= 0 && pos[j] < n;
+        wv[j] = live ? w[j] : 0.f;  // a slot without a row adds zero
+        v[j].clear();
+        if (live) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
       }
-    if (j0 == 0) {  // the addend is waited for after the rows are on their way
-#pragma unroll
-      for (int p = 0; p < P; p++) pa[p].get(acc[p]);
-    }
-#pragma unroll
-    for (int p = 0; p < P; p++)
+      if (j0 + U < a.k) slots(t, j0 + U); else slots(t + stride, 0);
+      if (j0 == 0) pa.get(acc);  // waited for after the rows are on their way
 #pragma unroll
       for (int j = 0; j < U; j++) {
         float f[8];
-        v[p][j].get(f);
+        v[j].get(f);
 #pragma unroll
-        for (int m = 0; m < 8; m++) acc[p][m] = fmaf(w[j], f[m], acc[p][m]);
+        for (int m = 0; m < 8; m++) acc[m] = fmaf(wv[j], f[m], acc[m]);
       }
-  }
-#pragma unroll
-  for (int p = 0; p < P; p++) {
-    if (i0 + p * step >= a.H) continue;
+    }
     Pack<TO> o;
-    o.put(acc[p]);
-    store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i0 + p * step, a.H, o);
+    o.put(acc);
+    store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i, a.H, o);
   }
 }
 
@@ -378,27 +374,22 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
   }
 }
 
-template <typename TY, typename TO, bool VEC, int U, int P>
-static cudaError_t launch_combine_up(const CombineArgs &a, cudaStream_t st) {
-  const int packs = (a.H + 7) / 8, per = (packs + P - 1) / P;
+template <typename TY, typename TO, bool VEC, int U>
+static cudaError_t launch_combine_u(const CombineArgs &a, cudaStream_t st) {
+  const int packs = (a.H + 7) / 8;
   int bx = 32;  // short rows: several tokens a CTA
-  while (bx < per && bx < kRowThreads) bx *= 2;
+  while (bx < packs && bx < kRowThreads) bx *= 2;
   const dim3 block(bx, kRowThreads / bx);
-  const dim3 grid((per + bx - 1) / bx, (a.T + block.y - 1) / block.y);
-  return launch_pdl(combine_rows_kernel<TY, TO, VEC, U, P>, grid, block, 0, st, a);
+  const int gx = (packs + bx - 1) / bx, rows = (a.T + block.y - 1) / block.y;
+  const int per_sm = U <= 2 ? 16 : 8;  // CTAs: enough to fill the SMs once or twice over
+  const dim3 grid(gx, std::min(rows, std::max(1, per_sm * dev_info().sms / gx)));
+  return launch_pdl(combine_rows_kernel<TY, TO, VEC, U>, grid, block, 0, st, a);
 }
 
 template <typename TY, typename TO, bool VEC>
 static cudaError_t launch_combine_v(const CombineArgs &a, cudaStream_t st) {
-  // enough rows to fill the GPU: more packs a thread where few slots are in flight
-  const bool many = (long)a.T * a.H >= (long)dev_info().sms * 2048 * 8 * 4;
-  if (a.k <= 2)
-    return many ? launch_combine_up<TY, TO, VEC, 2, 4>(a, st)
-                : launch_combine_up<TY, TO, VEC, 2, 1>(a, st);
-  if (a.k <= 4)
-    return many ? launch_combine_up<TY, TO, VEC, 4, 2>(a, st)
-                : launch_combine_up<TY, TO, VEC, 4, 1>(a, st);
-  return launch_combine_up<TY, TO, VEC, 8, 1>(a, st);
+  return a.k <= 2 ? launch_combine_u<TY, TO, VEC, 2>(a, st)
+                  : launch_combine_u<TY, TO, VEC, 4>(a, st);
 }
 
 template <typename TY, typename TO>
@@ -445,10 +436,9 @@ static cudaError_t launch_dispatch(int T, int k, int E, long row_bytes, long ldx
                                    void *xs, int SC, const float *sc, long ldsc, float *scs,
                                    cudaStream_t st) {
   const long units = row_bytes / (long)sizeof(W);
-  // few tokens: a row is shared by several warps, so that the copies spread over the SMs
-  const long chunks = std::max(1l, (units + 255) / 256);
-  const long target = 16l * dev_info().sms;
-  const int pieces = (int)std::min(chunks, std::max(1l, target / T));
+  // a warp moves a piece of 256 units of a row: the loads of eight a lane, then the stores of
+  // each slot (a whole row a warp: 155 us where pieces take 147, 8192 x 8 rows of 6144 bf16)
+  const int pieces = (int)std::max(1l, (units + 255) / 256);
   const long items = (long)T * pieces;
   const unsigned grid = (unsigned)std::min((items + kRowWarps - 1) / kRowWarps,
                                            (long)dev_info().sms * 64);
