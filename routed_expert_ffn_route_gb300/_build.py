@@ -1,5 +1,6 @@
 """Build the CUDA library in-tree: every csrc/*.cu compiled for sm_103a in parallel, then
-linked into libmoe_gb300.so next to this file.  No cmake; nvcc and a C++ host compiler only."""
+linked into libmoe_gb300.so next to this file, and the token operators' Python entry points
+(csrc/tokens_py.c).  No cmake; nvcc and a host compiler only."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,11 +9,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+PY_EXT = os.path.join(HERE, "_tokens_native.so")  # Python entry points of the token operators
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -65,7 +68,26 @@ def build(force: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    _python_entries(force)
     return LIB
+
+
+def _python_entries(force: bool):
+    """The token operators' CPython entry points, linked against the library beside them."""
+    src = os.path.join(CSRC, "tokens_py.c")
+    dep = max(os.path.getmtime(p) for p in [src, LIB] + _headers())
+    if os.path.exists(PY_EXT) and os.path.getmtime(PY_EXT) >= dep and not force:
+        return
+    tmp = PY_EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-Wno-missing-field-initializers",
+           "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-o", tmp, src, "-L", HERE,
+           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for tokens_py.c:\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, PY_EXT)
 
 
 if __name__ == "__main__":

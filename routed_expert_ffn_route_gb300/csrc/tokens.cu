@@ -41,6 +41,7 @@ struct SortShared {
   int total[kSortMaxE];                  // this CTA's slots per expert
   int start[kSortMaxE + 1];              // first position of each expert
   int base[kSortMaxE];                   // first position of each expert in this CTA
+  int warps[8];                          // slots of each 32 experts
 };
 
 constexpr int kSortBatch = 8;  // steps of 32 slots loaded at a time
@@ -98,39 +99,32 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
     S.total[x] = s;
   }
   if (ncta > 1) cl.sync(); else __syncthreads();
-  for (int x = tid; x < E; x += blockDim.x) {
-    int before = 0, all = 0;
+  // exclusive scan over the experts (at most 256, a thread each): within warps, then over them
+  int all = 0, before = 0;
+  if (tid < E) {
     for (int c = 0; c < ncta; c++) {
-      const int v = cl.map_shared_rank(S.total, c)[x];
+      const int v = ncta > 1 ? cl.map_shared_rank(S.total, c)[tid] : S.total[tid];
       if (c < rank) before += v;
       all += v;
     }
-    S.start[x] = all;
-    S.base[x] = before;
   }
-  __syncthreads();
-  if (warp == 0) {  // exclusive scan over the experts
-    const int per = (E + 31) / 32;
-    int s = 0;
-    for (int i = 0; i < per; i++)
-      if (lane * per + i < E) s += S.start[lane * per + i];
-    int incl = s;
+  int incl = all;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31 && warp < 8) S.warps[warp] = incl;
+  __syncthreads();
+  if (tid < kSortMaxE) {
+    int add = 0;
+#pragma unroll
+    for (int q = 0; q < 8; q++) add += q < warp ? S.warps[q] : 0;
+    if (tid < E) {
+      S.start[tid] = add + incl - all;
+      S.base[tid] = add + incl - all + before;
     }
-    int r = incl - s;
-    for (int i = 0; i < per; i++) {
-      const int x = lane * per + i;
-      if (x < E) {
-        const int c = S.start[x];
-        S.start[x] = r;
-        S.base[x] += r;
-        r += c;
-      }
-    }
-    if (lane == 31) S.start[E] = incl;
+    if (tid == E - 1) S.start[E] = add + incl;
   }
   __syncthreads();
   const bool once = hi - lo <= 32 * kSortBatch;  // the run's ids are still in registers

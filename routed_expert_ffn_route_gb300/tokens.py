@@ -6,8 +6,10 @@ kernels, on the current stream, into tensors that the caller owns; nothing is al
 every call may be captured into a graph.  Shapes, types, strides and devices are checked here
 (the C entry points see only addresses): a wrong one raises ValueError or TypeError.
 
-At decode sizes the host side of a call counts as much as its kernel, so the checks read each
-tensor attribute once and arguments go to the C entry points as plain integers.
+At decode sizes the host side of a call counts as much as its kernel: the checks read each
+tensor attribute once, and the arguments go to the C entry points as plain integers through a
+small extension module (csrc/tokens_py.c) instead of ctypes (5.3 us for a whole call of the norm
+where ctypes took 7.3).
 """
 from __future__ import annotations
 
@@ -15,20 +17,13 @@ import torch
 
 from . import MOE_DT_BF16, MOE_DT_E4M3, MOE_DT_F16, MOE_DT_F32, MOE_OK, MoEError, lib
 
+lib()  # raises if the library has not been built; the extension module is built with it
+from . import _tokens_native as _native  # noqa: E402
+
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 _F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
 _DTYPES = {_F32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16,
            _E4M3: MOE_DT_E4M3}
-
-_L = None
-
-
-def _lib():
-    global _L
-    if _L is None:
-        _L = lib()
-    return _L
-
 
 def _row_type(dtype) -> int:
     t = _DTYPES.get(dtype)
@@ -67,6 +62,8 @@ def _rows(t, shape, dtype, dev, name):
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
         _wrong(t, shape, dtype, dev, name)
     n = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), n
     ld, step = t.stride()
     if step != 1 and n > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -104,9 +101,9 @@ def moe_rmsnorm_e4m3(x, q, scale, add=None, weight=None, resid=None, eps=1e-6, g
     pa, lda = (None, 0) if add is None else _rows(add, shape, dt, dev, "add")
     pr, ldr = (None, 0) if resid is None else _rows(resid, shape, dt, dev, "resid")
     pw = None if weight is None else _flat(weight, (H,), dt, dev, "weight")
-    _check(_lib().moe_rmsnorm_e4m3(T, H, px, ldx, _row_type(dt), pa, lda, pw, eps,
-                                   1 if normalize else 0, group, pr, ldr, pq, ldq, ps,
-                                   _stream_of(dev, stream)), "moe_rmsnorm_e4m3")
+    _check(_native.rmsnorm(T, H, px, ldx, _row_type(dt), pa, lda, pw, eps,
+                           1 if normalize else 0, group, pr, ldr, pq, ldq, ps,
+                           _stream_of(dev, stream)), "moe_rmsnorm_e4m3")
 
 
 def moe_sort_tokens(ids, n_experts, offsets, perm, slot_pos, stream=None):
@@ -117,7 +114,7 @@ def moe_sort_tokens(ids, n_experts, offsets, perm, slot_pos, stream=None):
     po = _flat(offsets, (n_experts + 1,), _I32, dev, "offsets")
     pp = _flat(perm, (T * k,), _I32, dev, "perm")
     ps = _flat(slot_pos, shape, _I32, dev, "slot_pos")
-    _check(_lib().moe_sort_tokens(T, k, n_experts, pi, po, pp, ps, _stream_of(dev, stream)),
+    _check(_native.sort(T, k, n_experts, pi, po, pp, ps, _stream_of(dev, stream)),
            "moe_sort_tokens")
 
 
@@ -138,8 +135,8 @@ def moe_dispatch_rows(x, slot_pos, offsets, xs, scale=None, scale_s=None, stream
         if scale_s is None:
             raise ValueError("scale_s is needed with scale")
         pss = _flat(scale_s, (T * k, S), _F32, dev, "scale_s")
-    _check(_lib().moe_dispatch_rows(T, k, E1 - 1, H, _row_type(dt), px, ldx, pp, po, pxs, S, psc,
-                                    ldsc, pss, _stream_of(dev, stream)), "moe_dispatch_rows")
+    _check(_native.dispatch(T, k, E1 - 1, H, _row_type(dt), px, ldx, pp, po, pxs, S, psc,
+                            ldsc, pss, _stream_of(dev, stream)), "moe_dispatch_rows")
 
 
 def moe_combine_rows(y, slot_pos, out, w=None, add=None, stream=None):
@@ -151,8 +148,8 @@ def moe_combine_rows(y, slot_pos, out, w=None, add=None, stream=None):
     po, ldo = _rows(out, (T, H), ot, dev, "out")
     pa, lda = (None, 0) if add is None else _rows(add, (T, H), ot, dev, "add")
     pw = None if w is None else _flat(w, (T, k), _F32, dev, "w")
-    _check(_lib().moe_combine_rows(T, k, H, py, _row_type(yt), pp, pw, pa, lda, po, ldo,
-                                   _row_type(ot), _stream_of(dev, stream)), "moe_combine_rows")
+    _check(_native.combine(T, k, H, py, _row_type(yt), pp, pw, pa, lda, po, ldo,
+                           _row_type(ot), _stream_of(dev, stream)), "moe_combine_rows")
 
 
 def moe_combine_rows_grad(dout, y, slot_pos, offsets, w, dy, dw, stream=None):
@@ -166,8 +163,8 @@ def moe_combine_rows_grad(dout, y, slot_pos, offsets, w, dy, dw, stream=None):
     pp = _flat(slot_pos, (T, k), _I32, dev, "slot_pos")
     po = _flat(offsets, (E1,), _I32, dev, "offsets")
     pw = None if w is None else _flat(w, (T, k), _F32, dev, "w")
-    _check(_lib().moe_combine_rows_grad(T, k, E1 - 1, H, _row_type(dt), pd, ldd, py, pp, po, pw,
-                                        pdy, pdw, _stream_of(dev, stream)),
+    _check(_native.combine_grad(T, k, E1 - 1, H, _row_type(dt), pd, ldd, py, pp, po, pw,
+                                pdy, pdw, _stream_of(dev, stream)),
            "moe_combine_rows_grad")
 
 
@@ -178,8 +175,8 @@ def moe_dispatch_rows_grad(dxs, slot_pos, dx, stream=None):
     pd = _flat(dxs, (T * k, H), dt, dev, "dxs")
     pp = _flat(slot_pos, (T, k), _I32, dev, "slot_pos")
     px, ldx = _rows(dx, (T, H), xt, dev, "dx")
-    _check(_lib().moe_dispatch_rows_grad(T, k, H, _row_type(dt), pd, pp, px, ldx, _row_type(xt),
-                                         _stream_of(dev, stream)), "moe_dispatch_rows_grad")
+    _check(_native.dispatch_grad(T, k, H, _row_type(dt), pd, pp, px, ldx, _row_type(xt),
+                                 _stream_of(dev, stream)), "moe_dispatch_rows_grad")
 
 
 def moe_linear(x, w, out, x_scale=None, w_scale=None, bias=None, act="none", residual=None,
@@ -212,6 +209,6 @@ def moe_linear(x, w, out, x_scale=None, w_scale=None, bias=None, act="none", res
     pws = None if w_scale is None else _flat(w_scale, lead, _F32, dev, "w_scale")
     pb = None if bias is None else _flat(bias, lead, _F32, dev, "bias")
     pst = None if status is None else _flat(status, (1,), _I32, dev, "status")
-    _check(_lib().moe_linear(R, N, K, E, px, ldx, _row_type(dt), pxs, pw, pws, pb, code, pr, ldr,
-                             po, pout, ldo, _row_type(ot), pst, _stream_of(dev, stream)),
+    _check(_native.linear(R, N, K, E, px, ldx, _row_type(dt), pxs, pw, pws, pb, code, pr, ldr,
+                          po, pout, ldo, _row_type(ot), pst, _stream_of(dev, stream)),
            "moe_linear")

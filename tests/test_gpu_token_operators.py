@@ -513,3 +513,54 @@ def test_chain_repeats_bit_for_bit_on_a_stream_and_in_a_graph():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+def test_linear_on_two_streams_at_once():
+    """Calls of every form overlapping on two streams give the bits they give alone."""
+    shapes = [(1, 2048, 6144, 0, TB, "silu"), (16, 512, 1024, 0, F8, "none"),
+              (200, 1024, 2048, 0, TB, "none"), (1000, 1024, 512, 0, F8, "swiglu"),
+              (40, 256, 512, 16, F8, "swiglu"), (3000, 512, 1024, 4, TB, "none")]
+    calls = []
+    for i, (R, N, K, E, dt, act) in enumerate(shapes):
+        rows = 2 * N if act == "swiglu" else N
+        x, w = randn(i, R, K).to(dt), randn(i + 50, max(1, E), rows, K).to(dt)
+        off = None
+        if E:
+            off = torch.linspace(0, R, E + 1, device="cuda").int()
+        out = torch.empty(R, N, dtype=TB, device="cuda")
+        kw = dict(act=act, offsets=off)
+        moe.moe_linear(x, w if E else w[0], out, **kw)
+        calls.append((x, w if E else w[0], out.clone(), torch.empty_like(out),
+                      torch.empty_like(out), kw))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for s, st in enumerate(streams):
+            for x, w, _, o1, o2, kw in (calls if s == 0 else calls[::-1]):
+                moe.moe_linear(x, w, o1 if s == 0 else o2, stream=st, **kw)
+    torch.cuda.synchronize()
+    for _, _, want, o1, o2, _ in calls:
+        assert torch.equal(o1, want) and torch.equal(o2, want)
+
+
+def test_operators_follow_each_other_without_waiting():
+    """Each kernel may start while the one before it ends: weights and rows written by the call
+    just before are the ones that are read."""
+    R, N, K = 64, 256, 512
+    src = [randn(i, N, K) for i in range(6)]
+    x = randn(9, R, K)
+    q, s = torch.empty(N, K, dtype=F8, device="cuda"), torch.empty(N, 1, device="cuda")
+    xq, xs = torch.empty(R, K, dtype=F8, device="cuda"), torch.empty(R, 1, device="cuda")
+    outs = [torch.empty(R, N, device="cuda") for _ in src]
+    moe.moe_rmsnorm_e4m3(x, xq, xs, normalize=False)
+    for w, out in zip(src, outs):
+        moe.moe_rmsnorm_e4m3(w, q, s, normalize=False)
+        moe.moe_linear(xq, q, out, x_scale=xs, w_scale=s[:, 0])
+    torch.cuda.synchronize()
+    for w, out in zip(src, outs):
+        moe.moe_rmsnorm_e4m3(w, q, s, normalize=False)
+        torch.cuda.synchronize()
+        alone = torch.empty_like(out)
+        moe.moe_linear(xq, q, alone, x_scale=xs, w_scale=s[:, 0])
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone)
