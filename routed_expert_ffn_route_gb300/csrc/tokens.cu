@@ -164,9 +164,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(int n, int E,
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
+constexpr int kMoveThreads = 128;
+constexpr int kMoveWarps = kMoveThreads / 32;
+
 // Row copies move `U` units of W bytes a lane per step, all loads before the stores.
 template <typename W>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kMoveThreads)
     dispatch_kernel(int T, int k, int E, long units, long ldx, const W *x, const int32_t *slot_pos,
                     const int32_t *offsets, W *xs, int pieces, int SC, const float *sc, long ldsc,
                     float *scs) {
@@ -175,8 +178,8 @@ __global__ void __launch_bounds__(kRowThreads)
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const long n = (long)T * k;
-  const long nwarps = (long)gridDim.x * kRowWarps;
-  const long gw = (long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const long nwarps = (long)gridDim.x * kMoveWarps;
+  const long gw = (long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   for (long item = gw; item < (long)T * pieces; item += nwarps) {
     const long t = item / pieces;
     const int piece = (int)(item - t * pieces);
@@ -434,9 +437,9 @@ static cudaError_t launch_dispatch(int T, int k, int E, long row_bytes, long ldx
   // each slot (a whole row a warp: 155 us where pieces take 147, 8192 x 8 rows of 6144 bf16)
   const int pieces = (int)std::max(1l, (units + 255) / 256);
   const long items = (long)T * pieces;
-  const unsigned grid = (unsigned)std::min((items + kRowWarps - 1) / kRowWarps,
-                                           (long)dev_info().sms * 64);
-  return launch_pdl(dispatch_kernel<W>, dim3(std::max(1u, grid)), dim3(kRowThreads), 0, st, T, k,
+  const unsigned grid = (unsigned)std::min((items + kMoveWarps - 1) / kMoveWarps,
+                                           (long)dev_info().sms * 128);
+  return launch_pdl(dispatch_kernel<W>, dim3(std::max(1u, grid)), dim3(kMoveThreads), 0, st, T, k,
                     E, units, ldx_bytes / (long)sizeof(W), (const W *)x, slot_pos, offsets,
                     (W *)xs, pieces, SC, sc, ldsc, scs);
 }
