@@ -36,137 +36,141 @@ __device__ __forceinline__ float e4m3_factor(float a, float &scale) {
     scale = 0.f;
     return 0.f;
   }
-  scale = __fdiv_rn(a, kE4m3Max);
-  return __fdiv_rn(kE4m3Max, a);
+  scale = a * (1.0f / kE4m3Max);
+  return kE4m3Max * __frcp_rn(a);
 }
 
-// TPR threads per row (a multiple of 32, blockDim.x); ROWS > 1 only with one warp per row.
-// Thread t holds the packs t, t + TPR, ... (at most PACKS of them).  Maxima are taken on the
+// blockDim.x threads (whole warps) share a row; blockDim.y rows a CTA only with one warp a row.
+// Thread t holds the packs t, t + blockDim.x, ... (at most PACKS of them).  A CTA takes rows at a
+// stride, and loads the next one while it joins and encodes this one.  Maxima are taken on the
 // bit patterns of |v|, where NaN is largest, so a NaN shows in the scale.
 template <typename T, int PACKS, bool VEC>
 __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(const NormArgs a) {
   pdl_wait();
   pdl_trigger();
+  __shared__ float ps[2][32];
+  __shared__ uint32_t pm[2][32];
   const int tpr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= a.T) return;  // whole rows leave together (blockDim.y > 1: a row is one warp)
-  const T *x = (const T *)a.x + (size_t)t * a.ldx;
-  const T *add = a.add ? (const T *)a.add + (size_t)t * a.ldadd : nullptr;
-  T *resid = a.resid ? (T *)a.resid + (size_t)t * a.ldr : nullptr;
+  const int H = a.H, G = a.group, ng = G ? (H + G - 1) / G : 1;
   const T *w = (const T *)a.w;
-  const int H = a.H;
-
   Pack<T> px[PACKS], pa[PACKS];
+  auto load = [&](int t) {
+    const T *x = (const T *)a.x + (size_t)t * a.ldx;
+    const T *add = (const T *)a.add + (size_t)t * a.ldadd;
 #pragma unroll
-  for (int j = 0; j < PACKS; j++) {
-    const int i = 8 * (tid + j * tpr);
-    if (i < H) {
+    for (int j = 0; j < PACKS; j++) {
+      const int i = 8 * (tid + j * tpr);
+      if (i >= H) continue;
       px[j] = load_pack<T, VEC>(x, i, H);
-      if (add) pa[j] = load_pack<T, VEC>(add, i, H);
+      if (a.add) pa[j] = load_pack<T, VEC>(add, i, H);
     }
-  }
-  float v[PACKS][8];
-  uint32_t mx[PACKS];
-  float ss = 0.f;
-  uint32_t m = 0;
+  };
+  const int stride = gridDim.x * blockDim.y;
+  int t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t < a.T) load(t);
+  for (int par = 0; t < a.T; t += stride, par ^= 1) {
+    float v[PACKS][8];
+    uint32_t mx[PACKS], m = 0;
+    float ss = 0.f;
 #pragma unroll
-  for (int j = 0; j < PACKS; j++) {
-    const int i = 8 * (tid + j * tpr);
-    mx[j] = 0;
-    if (i >= H) continue;
-    px[j].get(v[j]);
-    if (add) {  // the sum is rounded to the row's type, and read as rounded
-      float av[8];
-      pa[j].get(av);
-#pragma unroll
-      for (int k = 0; k < 8; k++) v[j][k] += av[k];
-      px[j].put(v[j]);
+    for (int j = 0; j < PACKS; j++) {
+      const int i = 8 * (tid + j * tpr);
+      mx[j] = 0;
+      if (i >= H) continue;
       px[j].get(v[j]);
+      if (a.add) {  // the sum is rounded to the row's type, and read as rounded
+        float av[8];
+        pa[j].get(av);
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[j][k] += av[k];
+        px[j].put(v[j]);
+        px[j].get(v[j]);
+      }
+      if (a.resid) store_pack<T, VEC>((T *)a.resid + (size_t)t * a.ldr, i, H, px[j]);
+#pragma unroll
+      for (int k = 0; k < 8; k++) ss += v[j][k] * v[j][k];
+      if (w) {
+        float wv[8];
+        load_pack<T, VEC>(w, i, H).get(wv);
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[j][k] *= wv[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; k++) mx[j] = max(mx[j], __float_as_uint(fabsf(v[j][k])));
+      m = max(m, mx[j]);
     }
-    if (resid) store_pack<T, VEC>(resid, i, H, px[j]);
-#pragma unroll
-    for (int k = 0; k < 8; k++) ss += v[j][k] * v[j][k];
-    if (w) {
-      float wv[8];
-      load_pack<T, VEC>(w, i, H).get(wv);
-#pragma unroll
-      for (int k = 0; k < 8; k++) v[j][k] *= wv[k];
+    if (t + stride < a.T) load(t + stride);
+    ss = warp_sum(ss);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (tpr > 32) {  // two sets of sums in turn: one barrier a row keeps them apart
+      if (lane == 0) ps[par][warp] = ss, pm[par][warp] = m;
+      __syncthreads();
+      const int nw = tpr >> 5;
+      ss = warp_sum(lane < nw ? ps[par][lane] : 0.f);
+      m = __reduce_max_sync(0xffffffffu, lane < nw ? pm[par][lane] : 0u);
     }
+    const float inv = a.normalize ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
+    float *scale = a.scale + (size_t)t * ng;
+    float f, s;
+    if (!G) {
+      f = e4m3_factor(__uint_as_float(m) * inv, s);
+      if (tid == 0) scale[0] = s;
+    }
+    uint8_t *q = a.q + (size_t)t * a.ldq;
 #pragma unroll
-    for (int k = 0; k < 8; k++) mx[j] = max(mx[j], __float_as_uint(fabsf(v[j][k])));
-    m = max(m, mx[j]);
+    for (int j = 0; j < PACKS; j++) {
+      const int i = 8 * (tid + j * tpr);
+      if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
+        uint32_t gm = mx[j];
+        for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+        f = e4m3_factor(__uint_as_float(gm) * inv, s);
+        if (i < H && i % G == 0) scale[i / G] = s;
+      }
+      if (i >= H) continue;
+      uint16_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
+        c[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+      }
+      if (VEC) {
+        *(uint2 *)(q + i) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+          if (i + k < H) q[i + k] = (uint8_t)(c[k >> 1] >> (8 * (k & 1)));
+      }
+    }
   }
-  ss = warp_sum(ss);
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (tpr > 32) {
-    __shared__ float ps[32];
-    __shared__ uint32_t pm[32];
-    if (lane == 0) ps[warp] = ss, pm[warp] = m;
-    __syncthreads();
-    const int nw = tpr >> 5;
-    ss = warp_sum(lane < nw ? ps[lane] : 0.f);
-    m = __reduce_max_sync(0xffffffffu, lane < nw ? pm[lane] : 0u);
-  }
-  const float inv = a.normalize ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
-  const int G = a.group, ng = G ? (H + G - 1) / G : 1;
-  float *scale = a.scale + (size_t)t * ng;
-  float f, s;
-  if (!G) {
-    f = e4m3_factor(__uint_as_float(m) * inv, s);
-    if (tid == 0) scale[0] = s;
-  }
-  uint8_t *q = a.q + (size_t)t * a.ldq;
-#pragma unroll
-  for (int j = 0; j < PACKS; j++) {
-    const int i = 8 * (tid + j * tpr);
-    if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
-      uint32_t gm = mx[j];
-      for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-      f = e4m3_factor(__uint_as_float(gm) * inv, s);
-      if (i < H && i % G == 0) scale[i / G] = s;
-    }
-    if (i >= H) continue;
-    uint16_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
-      c[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-    }
-    if (VEC) {
-      *(uint2 *)(q + i) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; k++)
-        if (i + k < H) q[i + k] = (uint8_t)(c[k >> 1] >> (8 * (k & 1)));
-    }
-  }
+}
+
+template <typename T, int PACKS, bool VEC>
+static cudaError_t launch_norm_p(const NormArgs &a, dim3 block, cudaStream_t st) {
+  auto *k = rmsnorm_e4m3_kernel<T, PACKS, VEC>;
+  const int rows = (a.T + block.y - 1) / block.y;
+  const int fit = std::max(1, cached_blocks_per_sm((const void *)k, block.x * block.y, 0));
+  return launch_pdl(k, dim3(std::min(rows, fit * dev_info().sms)), block, 0, st, a);
 }
 
 template <typename T, bool VEC>
 static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
   const int packs = (a.H + 7) / 8;
   if (packs <= 128) {  // one warp a row, four rows a CTA: nothing to exchange between warps
-    const dim3 grid((a.T + 3) / 4), block(32, 4);
-    if (packs <= 32) return launch_pdl(rmsnorm_e4m3_kernel<T, 1, VEC>, grid, block, 0, st, a);
-    if (packs <= 64) return launch_pdl(rmsnorm_e4m3_kernel<T, 2, VEC>, grid, block, 0, st, a);
-    return launch_pdl(rmsnorm_e4m3_kernel<T, 4, VEC>, grid, block, 0, st, a);
+    const dim3 block(32, 4);
+    if (packs <= 32) return launch_norm_p<T, 1, VEC>(a, block, st);
+    if (packs <= 64) return launch_norm_p<T, 2, VEC>(a, block, st);
+    return launch_norm_p<T, 4, VEC>(a, block, st);
   }
-  // few rows: as many threads as the row has packs (the shortest path through one row); many
-  // rows: three packs a thread (8192 x 6144 bf16 with residual: one 80 us, two 68, three 62,
-  // four 66: fewer leave fewer loads in flight a thread, more take registers from other rows)
   auto threads = [&](int p) { return ((packs + p - 1) / p + 31) / 32 * 32; };
-  const bool few = a.T <= 2 * dev_info().sms;
-  const int per = few && threads(1) <= 1024   ? 1
-                  : few && threads(2) <= 1024 ? 2
-                  : threads(3) <= 512         ? 3
-                  : threads(4) <= 512         ? 4
-                                              : 8;
-  const dim3 grid(a.T), block(threads(per));
-  if (per == 1) return launch_pdl(rmsnorm_e4m3_kernel<T, 1, VEC>, grid, block, 0, st, a);
-  if (per == 2) return launch_pdl(rmsnorm_e4m3_kernel<T, 2, VEC>, grid, block, 0, st, a);
-  if (per == 3) return launch_pdl(rmsnorm_e4m3_kernel<T, 3, VEC>, grid, block, 0, st, a);
-  if (per == 4) return launch_pdl(rmsnorm_e4m3_kernel<T, 4, VEC>, grid, block, 0, st, a);
-  return launch_pdl(rmsnorm_e4m3_kernel<T, 8, VEC>, grid, block, 0, st, a);
+  // Few rows: as many threads as the row has packs, the shortest path through one row.  Many
+  // rows: two packs a thread (8192 x 6144 bf16 with residual: one 71 us, two 55, three 75, four
+  // 63: fewer leave fewer loads in flight, more take the registers of other rows; fp32, twice
+  // the bytes a pack: one 104 us, two 111).
+  const bool one = a.T <= 2 * dev_info().sms || sizeof(T) == 4;
+  if (one && threads(1) <= 1024) return launch_norm_p<T, 1, VEC>(a, dim3(threads(1)), st);
+  if (threads(2) <= (one ? 1024 : 512)) return launch_norm_p<T, 2, VEC>(a, dim3(threads(2)), st);
+  if (threads(4) <= 512) return launch_norm_p<T, 4, VEC>(a, dim3(threads(4)), st);
+  return launch_norm_p<T, 8, VEC>(a, dim3(threads(8)), st);
 }
 
 template <typename T>

@@ -233,9 +233,12 @@ struct CombineArgs {
 // (and the addend) in flight at a time, the next token's slots loaded meanwhile, so that only
 // the first token waits for slots before its rows; fp32 sum in slot order, one rounding.
 // 8192 tokens x 8 of 6144 bf16: 151 us, 6.7 TB/s (a CTA per token and eight slots in flight:
-// 184; four 169); x 2 of 4096: 49 us, 5.5 TB/s (two to four tokens or packs a thread: 48 to 61).
+// 184; four 169); x 2 of 4096: 45 us, 5.9 TB/s (two to four tokens or packs a thread: 48 to 61).
+// Two slots of 16-bit rows are few bytes a thread: six CTAs an SM (40 registers a thread) take 45
+// us where five take 49; more bytes a thread want the registers (four slots: 171 us against 151).
 template <typename TY, typename TO, bool VEC, int U>
-__global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const CombineArgs a) {
+__global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4)
+    combine_rows_kernel(const CombineArgs a) {
   pdl_wait();
   pdl_trigger();
   const int i = 8 * (int)(blockIdx.x * blockDim.x + threadIdx.x);
