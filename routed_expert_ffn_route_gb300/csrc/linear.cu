@@ -283,7 +283,7 @@ struct LinOut {
     for (int i = 0; i < IT; i++) {
       if (c0 + i * RPI + lane / LPR >= end) continue;
       const TO *r = rp + (long)(c0 + i * RPI) * ldres;
-      rv[i] = vec ? load_pack<TO, true>(r, 0, 8) : load_pack<TO, false>(r, 0, nf);
+      rv[i] = vec ? load_pack<TO, kVec>(r, 0, 8) : load_run<TO>(r, nf);
     }
   }
 
@@ -329,8 +329,8 @@ struct LinOut {
         Pack<TO> o;
         o.put(y);
         TO *d = op + (long)(c0 + i * RPI) * ldout;
-        if (vec) store_pack<TO, true>(d, 0, 8, o);
-        else store_pack<TO, false>(d, 0, nf, o);
+        if (vec) store_pack<TO, kVec>(d, 0, 8, o);
+        else store_run<TO>(d, nf, o);
       }
     }
     __syncwarp();
@@ -637,8 +637,8 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
     for (int i = blockIdx.x; i < rest; i += gridDim.x) {
       TO *row = (TO *)a.out + (long)(i < lead ? i : b->off[a.E] + i - lead) * a.ldout;
       for (int f = 8 * (tid - 64); f < a.N; f += 8 * 32 * kLinEpi) {
-        if (a.vec && f + 8 <= a.N) store_pack<TO, true>(row, f, a.N, zero);
-        else store_pack<TO, false>(row, f, a.N, zero);
+        if (a.vec && f + 8 <= a.N) store_pack<TO, kVec>(row, f, a.N, zero);
+        else store_run<TO>(row + f, a.N - f, zero);
       }
     }
   }

@@ -44,7 +44,7 @@ __device__ __forceinline__ float e4m3_factor(float a, float &scale) {
 // Thread t holds the packs t, t + blockDim.x, ... (at most PACKS of them).  A CTA takes rows at a
 // stride, and loads the next one while it joins and encodes this one.  Maxima are taken on the
 // bit patterns of |v|, where NaN is largest, so a NaN shows in the scale.
-template <typename T, int PACKS, bool VEC>
+template <typename T, int PACKS, int A>
 __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(const NormArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -60,9 +60,9 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
 #pragma unroll
     for (int j = 0; j < PACKS; j++) {
       const int i = 8 * (tid + j * tpr);
-      if (i >= H) continue;
-      px[j] = load_pack<T, VEC>(x, i, H);
-      if (a.add) pa[j] = load_pack<T, VEC>(add, i, H);
+      if (Place<T, A>::first(i) >= H) continue;
+      px[j] = load_pack<T, A>(x, i, H);
+      if (a.add) pa[j] = load_pack<T, A>(add, i, H);
     }
   };
   const int stride = gridDim.x * blockDim.y;
@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
     for (int j = 0; j < PACKS; j++) {
       const int i = 8 * (tid + j * tpr);
       mx[j] = 0;
-      if (i >= H) continue;
+      if (A == kWord) {  // every lane's words take part in the groups' maxima
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[j][k] = 0.f;
+      }
+      if (Place<T, A>::first(i) >= H) continue;
       px[j].get(v[j]);
       if (a.add) {  // the sum is rounded to the row's type, and read as rounded
         float av[8];
@@ -86,12 +90,12 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
         px[j].put(v[j]);
         px[j].get(v[j]);
       }
-      if (a.resid) store_pack<T, VEC>((T *)a.resid + (size_t)t * a.ldr, i, H, px[j]);
+      if (a.resid) store_pack<T, A>((T *)a.resid + (size_t)t * a.ldr, i, H, px[j]);
 #pragma unroll
       for (int k = 0; k < 8; k++) ss += v[j][k] * v[j][k];
       if (w) {
         float wv[8];
-        load_pack<T, VEC>(w, i, H).get(wv);
+        load_pack<T, A>(w, i, H).get(wv);
 #pragma unroll
         for (int k = 0; k < 8; k++) v[j][k] *= wv[k];
       }
@@ -120,46 +124,90 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
 #pragma unroll
     for (int j = 0; j < PACKS; j++) {
       const int i = 8 * (tid + j * tpr);
-      if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
-        uint32_t gm = mx[j];
-        for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-        f = e4m3_factor(__uint_as_float(gm) * inv, s);
-        if (i < H && i % G == 0) scale[i / G] = s;
-      }
-      if (i >= H) continue;
-      uint16_t c[4];
+      const int e = Place<T, A>::first(i);
+      if (A != kWord) {
+        if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
+          uint32_t gm = mx[j];
+          for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+          f = e4m3_factor(__uint_as_float(gm) * inv, s);
+          if (i < H && i % G == 0) scale[i / G] = s;
+        }
+        if (i >= H) continue;
+        uint16_t c[4];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
-        c[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-      }
-      if (VEC) {
-        *(uint2 *)(q + i) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
-      } else {
+        for (int k = 0; k < 4; k++) {
+          const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
+          c[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+        }
+        if (A == kVec) {
+          *(uint2 *)(q + i) = make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-          if (i + k < H) q[i + k] = (uint8_t)(c[k >> 1] >> (8 * (k & 1)));
+          for (int k = 0; k < 8; k++)
+            if (i + k < H) q[i + k] = (uint8_t)(c[k >> 1] >> (8 * (k & 1)));
+        }
+      } else {  // word k of every lane is SPAN elements: half a group of 64, a group of 32, ...
+        constexpr int W = Pack<T>::W, PER = Place<T, A>::PER, SPAN = Place<T, A>::SPAN;
+        uint32_t gm[W];
+        if (G) {
+#pragma unroll
+          for (int k = 0; k < W; k++) {
+            uint32_t b = __float_as_uint(fabsf(v[j][PER * k]));
+            if (PER == 2) b = max(b, __float_as_uint(fabsf(v[j][PER * k + PER - 1])));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {  // lanes of one group: G / PER, at most the warp
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, b, o);
+              if (PER * o < G) b = max(b, other);
+            }
+            gm[k] = b;
+          }
+#pragma unroll
+          for (int o = 1; o < W; o <<= 1)
+            if (G > SPAN * o) {
+#pragma unroll
+              for (int k = 0; k < W; k += 2 * o) {
+                const uint32_t both = max(gm[k], gm[k + o]);
+#pragma unroll
+                for (int d = 0; d < 2 * o; d++) gm[k + d] = both;
+              }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+          const int at = e + SPAN * k;
+          if (G) {
+            f = e4m3_factor(__uint_as_float(gm[k]) * inv, s);
+            if (at < H && at % G == 0) scale[at / G] = s;
+          }
+          if (at >= H) continue;
+          if (PER == 2) {
+            const float2 y = make_float2(v[j][2 * k] * inv * f, v[j][2 * k + 1] * inv * f);
+            *(uint16_t *)(q + at) = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+          } else {
+            q[at] = __nv_cvt_float_to_fp8(v[j][k] * inv * f, __NV_SATFINITE, __NV_E4M3);
+          }
+        }
       }
     }
   }
 }
 
-template <typename T, int PACKS, bool VEC>
+template <typename T, int PACKS, int A>
 static cudaError_t launch_norm_p(const NormArgs &a, dim3 block, cudaStream_t st) {
-  auto *k = rmsnorm_e4m3_kernel<T, PACKS, VEC>;
+  auto *k = rmsnorm_e4m3_kernel<T, PACKS, A>;
   const int rows = (a.T + block.y - 1) / block.y;
   const int fit = std::max(1, cached_blocks_per_sm((const void *)k, block.x * block.y, 0));
   return launch_pdl(k, dim3(std::min(rows, fit * dev_info().sms)), block, 0, st, a);
 }
 
-template <typename T, bool VEC>
+template <typename T, int A>
 static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
   const int packs = (a.H + 7) / 8;
   if (packs <= 128) {  // one warp a row, four rows a CTA: nothing to exchange between warps
     const dim3 block(32, 4);
-    if (packs <= 32) return launch_norm_p<T, 1, VEC>(a, block, st);
-    if (packs <= 64) return launch_norm_p<T, 2, VEC>(a, block, st);
-    return launch_norm_p<T, 4, VEC>(a, block, st);
+    if (packs <= 32) return launch_norm_p<T, 1, A>(a, block, st);
+    if (packs <= 64) return launch_norm_p<T, 2, A>(a, block, st);
+    return launch_norm_p<T, 4, A>(a, block, st);
   }
   auto threads = [&](int p) { return ((packs + p - 1) / p + 31) / 32 * 32; };
   // Few rows: as many threads as the row has packs, the shortest path through one row.  Many
@@ -167,10 +215,10 @@ static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
   // 63: fewer leave fewer loads in flight, more take the registers of other rows; fp32, twice
   // the bytes a pack: one 104 us, two 111).
   const bool one = a.T <= 2 * dev_info().sms || sizeof(T) == 4;
-  if (one && threads(1) <= 1024) return launch_norm_p<T, 1, VEC>(a, dim3(threads(1)), st);
-  if (threads(2) <= (one ? 1024 : 512)) return launch_norm_p<T, 2, VEC>(a, dim3(threads(2)), st);
-  if (threads(4) <= 512) return launch_norm_p<T, 4, VEC>(a, dim3(threads(4)), st);
-  return launch_norm_p<T, 8, VEC>(a, dim3(threads(8)), st);
+  if (one && threads(1) <= 1024) return launch_norm_p<T, 1, A>(a, dim3(threads(1)), st);
+  if (threads(2) <= (one ? 1024 : 512)) return launch_norm_p<T, 2, A>(a, dim3(threads(2)), st);
+  if (threads(4) <= 512) return launch_norm_p<T, 4, A>(a, dim3(threads(4)), st);
+  return launch_norm_p<T, 8, A>(a, dim3(threads(8)), st);
 }
 
 template <typename T>
@@ -178,8 +226,13 @@ static cudaError_t launch_norm_t(const NormArgs &a, cudaStream_t st) {
   const uintptr_t p = (uintptr_t)a.x | (uintptr_t)a.add | (uintptr_t)a.w | (uintptr_t)a.resid |
                       (uintptr_t)(a.ldx * sizeof(T)) | (uintptr_t)(a.ldadd * sizeof(T)) |
                       (uintptr_t)(a.ldr * sizeof(T));
-  const bool vec = p % 16 == 0 && a.H % 8 == 0 && ((uintptr_t)a.q | (uintptr_t)a.ldq) % 8 == 0;
-  return vec ? launch_norm<T, true>(a, st) : launch_norm<T, false>(a, st);
+  int acc = access_of(p, a.H, sizeof(T));
+  const uintptr_t pq = (uintptr_t)a.q | (uintptr_t)a.ldq;
+  if (acc == kVec && pq % 8) acc = kWord;
+  if (acc == kWord && sizeof(T) == 2 && pq % 2) acc = kAny;  // codes move two at a time
+  return acc == kVec    ? launch_norm<T, kVec>(a, st)
+         : acc == kWord ? launch_norm<T, kWord>(a, st)
+                        : launch_norm<T, kAny>(a, st);
 }
 
 }  // namespace moe

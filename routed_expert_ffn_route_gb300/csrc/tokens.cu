@@ -236,7 +236,7 @@ struct CombineArgs {
 // 184; four 169); x 2 of 4096: 45 us, 5.9 TB/s (two to four tokens or packs a thread: 48 to 61).
 // Two slots of 16-bit rows are few bytes a thread: six CTAs an SM (40 registers a thread) take 45
 // us where five take 49; more bytes a thread want the registers (four slots: 171 us against 151).
-template <typename TY, typename TO, bool VEC, int U>
+template <typename TY, typename TO, int A, int U>
 __global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4)
     combine_rows_kernel(const CombineArgs a) {
   pdl_wait();
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4
   const int i = 8 * (int)(blockIdx.x * blockDim.x + threadIdx.x);
   const int stride = gridDim.y * blockDim.y;
   int t = blockIdx.y * blockDim.y + threadIdx.y;
-  if (t >= a.T || i >= a.H) return;
+  if (t >= a.T || Place<TO, A>::first(i) >= a.H) return;
   const int n = a.T * a.k;
   const TY *y = (const TY *)a.y;
   int pos[U];
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4
   for (; t < a.T; t += stride) {
     Pack<TO> pa;
     pa.clear();
-    if (a.add) pa = load_pack<TO, VEC>((const TO *)a.add + t * a.ldadd, i, a.H);
+    if (a.add) pa = load_pack<TO, A>((const TO *)a.add + t * a.ldadd, i, a.H);
     float acc[8];
     for (int j0 = 0; j0 < a.k; j0 += U) {
       Pack<TY> v[U];
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4
         const bool live = pos[j] >= 0 && pos[j] < n;
         wv[j] = live ? w[j] : 0.f;  // a slot without a row adds zero
         v[j].clear();
-        if (live) v[j] = load_pack<TY, VEC>(y + (long)pos[j] * a.H, i, a.H);
+        if (live) v[j] = load_pack<TY, A>(y + (long)pos[j] * a.H, i, a.H);
       }
       if (j0 + U < a.k) slots(t, j0 + U); else slots(t + stride, 0);
       if (j0 == 0) pa.get(acc);  // waited for after the rows are on their way
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kRowThreads, U <= 2 && sizeof(TY) == 2 ? 6 : 4
     }
     Pack<TO> o;
     o.put(acc);
-    store_pack<TO, VEC>((TO *)a.out + t * a.ldout, i, a.H, o);
+    store_pack<TO, A>((TO *)a.out + t * a.ldout, i, a.H, o);
   }
 }
 
@@ -303,7 +303,7 @@ struct GradArgs {
 // A CTA per token: its dout pack stays in registers for the k slots (KC of them at a time),
 // whose y rows are read for dw and whose dy rows are written.  dw is summed over lanes, then
 // over warps, in a fixed order.  CTAs past the tokens write the zero rows of the tail.
-template <typename T, bool VEC, int KC>
+template <typename T, int A, int KC>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
     Pack<T> zero;
     zero.clear();
     for (long p = live + (blockIdx.x - a.T); p < n; p += gridDim.x - a.T)
-      for (int i = 8 * tid; i < a.H; i += 8 * blockDim.x)
-        store_pack<T, VEC>(dy + p * a.H, i, a.H, zero);
+      for (int i = 8 * tid; Place<T, A>::first(i) < a.H; i += 8 * blockDim.x)
+        store_pack<T, A>(dy + p * a.H, i, a.H, zero);
     return;
   }
   const long t = blockIdx.x;
@@ -334,13 +334,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
       w[j] = in ? a.w ? a.w[t * a.k + j0 + j] : 1.0f : 0.f;
       acc[j] = 0.f;
     }
-    for (int i = 8 * tid; i < a.H; i += 8 * blockDim.x) {
-      const Pack<T> pd = load_pack<T, VEC>(dout, i, a.H);
+    for (int i = 8 * tid; Place<T, A>::first(i) < a.H; i += 8 * blockDim.x) {
+      const Pack<T> pd = load_pack<T, A>(dout, i, a.H);
       Pack<T> py[KC];
 #pragma unroll
       for (int j = 0; j < KC; j++) {
         py[j].clear();
-        if (pos[j] >= 0) py[j] = load_pack<T, VEC>(y + (long)pos[j] * a.H, i, a.H);
+        if (pos[j] >= 0) py[j] = load_pack<T, A>(y + (long)pos[j] * a.H, i, a.H);
       }
       float d[8];
       pd.get(d);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
         }
         Pack<T> o;
         o.put(g);
-        store_pack<T, VEC>(dy + (long)pos[j] * a.H, i, a.H, o);
+        store_pack<T, A>(dy + (long)pos[j] * a.H, i, a.H, o);
       }
     }
     if (j0) __syncthreads();  // the last slots' sums have been read
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const GradArg
   }
 }
 
-template <typename TY, typename TO, bool VEC, int U>
+template <typename TY, typename TO, int A, int U>
 static cudaError_t launch_combine_u(const CombineArgs &a, cudaStream_t st) {
   const int packs = (a.H + 7) / 8;
   int bx = 32;  // short rows: several tokens a CTA
@@ -383,37 +383,43 @@ static cudaError_t launch_combine_u(const CombineArgs &a, cudaStream_t st) {
   const int gx = (packs + bx - 1) / bx, rows = (a.T + block.y - 1) / block.y;
   const int per_sm = U <= 2 ? 16 : 8;  // CTAs: enough to fill the SMs once or twice over
   const dim3 grid(gx, std::min(rows, std::max(1, per_sm * dev_info().sms / gx)));
-  return launch_pdl(combine_rows_kernel<TY, TO, VEC, U>, grid, block, 0, st, a);
+  return launch_pdl(combine_rows_kernel<TY, TO, A, U>, grid, block, 0, st, a);
 }
 
-template <typename TY, typename TO, bool VEC>
+template <typename TY, typename TO, int A>
 static cudaError_t launch_combine_v(const CombineArgs &a, cudaStream_t st) {
-  return a.k <= 2 ? launch_combine_u<TY, TO, VEC, 2>(a, st)
-                  : launch_combine_u<TY, TO, VEC, 4>(a, st);
+  return a.k <= 2 ? launch_combine_u<TY, TO, A, 2>(a, st)
+                  : launch_combine_u<TY, TO, A, 4>(a, st);
 }
 
 template <typename TY, typename TO>
 static cudaError_t launch_combine_rows(const CombineArgs &a, cudaStream_t st) {
   const uintptr_t p = (uintptr_t)a.y | (uintptr_t)a.add | (uintptr_t)a.out |
                       (uintptr_t)(a.ldadd * sizeof(TO)) | (uintptr_t)(a.ldout * sizeof(TO));
-  return p % 16 == 0 && a.H % 8 == 0 ? launch_combine_v<TY, TO, true>(a, st)
-                                     : launch_combine_v<TY, TO, false>(a, st);
+  const int acc = access_of(p, a.H, sizeof(TY));
+  if (acc == kVec) return launch_combine_v<TY, TO, kVec>(a, st);
+  // the words of a pack are the same elements only where both types have one size
+  constexpr int W = sizeof(TY) == sizeof(TO) ? kWord : kAny;
+  return acc == kWord ? launch_combine_v<TY, TO, W>(a, st) : launch_combine_v<TY, TO, kAny>(a, st);
 }
 
-template <typename T, bool VEC>
+template <typename T, int A>
 static cudaError_t launch_grad(const GradArgs &a, cudaStream_t st) {
   const int packs = (a.H + 7) / 8;
   const dim3 block(std::min(kRowThreads, (packs + 31) / 32 * 32));
   const dim3 grid(a.T + std::min(a.T, 2 * dev_info().sms));
-  if (a.k <= 2) return launch_pdl(combine_grad_kernel<T, VEC, 2>, grid, block, 0, st, a);
-  return launch_pdl(combine_grad_kernel<T, VEC, 4>, grid, block, 0, st, a);
+  if (a.k <= 2) return launch_pdl(combine_grad_kernel<T, A, 2>, grid, block, 0, st, a);
+  return launch_pdl(combine_grad_kernel<T, A, 4>, grid, block, 0, st, a);
 }
 
 template <typename T>
 static cudaError_t launch_grad_t(const GradArgs &a, cudaStream_t st) {
   const uintptr_t p = (uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy |
                       (uintptr_t)(a.lddout * sizeof(T));
-  return p % 16 == 0 && a.H % 8 == 0 ? launch_grad<T, true>(a, st) : launch_grad<T, false>(a, st);
+  const int acc = access_of(p, a.H, sizeof(T));
+  return acc == kVec    ? launch_grad<T, kVec>(a, st)
+         : acc == kWord ? launch_grad<T, kWord>(a, st)
+                        : launch_grad<T, kAny>(a, st);
 }
 
 static bool float_type(int dt) {

@@ -60,7 +60,7 @@ def check_norm(x, add, w, eps, group, normalize, q, scale, resid):
 
 
 @pytest.mark.parametrize("dtype", [TB, TH, T32])
-@pytest.mark.parametrize("T,H", [(1, 1), (1, 6144), (3, 7), (5, 33), (2, 64), (9, 255), (300, 256),
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 6144), (3, 7), (5, 33), (2, 64), (9, 255), (3, 34), (5, 254), (2, 514), (310, 2052), (300, 256),
                                  (7, 520), (5, 1000), (4, 1024), (700, 1032), (3, 2050),
                                  (400, 4096), (2, 8200), (310, 8200), (2, 16384), (310, 16384),
                                  (3, 16392), (2, 32768), (310, 32768), (2, 32767)])
@@ -212,8 +212,8 @@ def combine_ref(y, pos, w, add, H):
     return out, mag
 
 
-@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 1), (1, 8, 256, 6144), (5, 2, 8, 33),
-                                     (33, 16, 64, 136), (64, 9, 40, 520), (200, 4, 16, 2050),
+@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 1), (1, 8, 256, 6144), (5, 2, 8, 33), (7, 3, 8, 34),
+                                     (90, 4, 8, 518), (33, 16, 64, 136), (64, 9, 40, 520), (200, 4, 16, 2050),
                                      (1031, 2, 8, 4096)])
 @pytest.mark.parametrize("dt,od", [(T32, T32), (TB, TB), (TB, T32), (TH, TH), (TH, T32)])
 @pytest.mark.parametrize("drop", [0.0, 0.4, 1.0])
