@@ -26,7 +26,7 @@ struct NormArgs {
   uint8_t *q;
   float *scale;
   long ldx, ldadd, ldr, ldq;
-  int T, H, group, normalize;
+  int T, H, group, gshift, normalize;  // group = 1 << gshift, or 0
   float eps;
 };
 
@@ -40,18 +40,26 @@ __device__ __forceinline__ float e4m3_factor(float a, float &scale) {
   return kE4m3Max * __frcp_rn(a);
 }
 
+// most threads of a CTA with `packs` packs a thread (three such CTAs of 16-bit rows fit an SM)
+constexpr int norm_threads(int packs, int size) {
+  return packs == 1 ? 1024 : packs == 2 ? (size == 2 ? 384 : 1024) : 512;
+}
+
 // blockDim.x threads (whole warps) share a row; blockDim.y rows a CTA only with one warp a row.
 // Thread t holds the packs t, t + blockDim.x, ... (at most PACKS of them).  A CTA takes rows at a
 // stride, and loads the next one while it joins and encodes this one.  Maxima are taken on the
 // bit patterns of |v|, where NaN is largest, so a NaN shows in the scale.
-template <typename T, int PACKS, int A>
-__global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(const NormArgs a) {
+// GROUPED: scales by group (a scale a row needs fewer registers, which wide rows want).
+template <typename T, int PACKS, int A, bool GROUPED>
+__global__ void __launch_bounds__(norm_threads(PACKS, sizeof(T)),
+                                  PACKS == 2 && sizeof(T) == 2 ? 3 : 1)
+    rmsnorm_e4m3_kernel(const NormArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ float ps[2][32];
   __shared__ uint32_t pm[2][32];
   const int tpr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int H = a.H, G = a.group, ng = G ? (H + G - 1) / G : 1;
+  const int H = a.H, G = GROUPED ? a.group : 0, ng = GROUPED ? (H + G - 1) / G : 1;
   const T *w = (const T *)a.w;
   Pack<T> px[PACKS], pa[PACKS];
   auto load = [&](int t) {
@@ -116,9 +124,18 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
     const float inv = a.normalize ? 1.0f / sqrtf(ss / (float)H + a.eps) : 1.0f;
     float *scale = a.scale + (size_t)t * ng;
     float f, s;
-    if (!G) {
+    if (!GROUPED) {
       f = e4m3_factor(__uint_as_float(m) * inv, s);
       if (tid == 0) scale[0] = s;
+    }
+    if (A != kWord && GROUPED) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (8 * o >= G) break;
+#pragma unroll
+        for (int j = 0; j < PACKS; j++)
+          mx[j] = max(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+      }
     }
     uint8_t *q = a.q + (size_t)t * a.ldq;
 #pragma unroll
@@ -126,11 +143,9 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
       const int i = 8 * (tid + j * tpr);
       const int e = Place<T, A>::first(i);
       if (A != kWord) {
-        if (G) {  // a group is G / 8 neighbouring lanes; lanes past the row hold zero
-          uint32_t gm = mx[j];
-          for (int o = 1; o < G / 8; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-          f = e4m3_factor(__uint_as_float(gm) * inv, s);
-          if (i < H && i % G == 0) scale[i / G] = s;
+        if (GROUPED) {
+          f = e4m3_factor(__uint_as_float(mx[j]) * inv, s);
+          if (i < H && (i & (G - 1)) == 0) scale[i >> a.gshift] = s;
         }
         if (i >= H) continue;
         uint16_t c[4];
@@ -149,7 +164,7 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
       } else {  // word k of every lane is SPAN elements: half a group of 64, a group of 32, ...
         constexpr int W = Pack<T>::W, PER = Place<T, A>::PER, SPAN = Place<T, A>::SPAN;
         uint32_t gm[W];
-        if (G) {
+        if (GROUPED) {
 #pragma unroll
           for (int k = 0; k < W; k++) {
             uint32_t b = __float_as_uint(fabsf(v[j][PER * k]));
@@ -175,9 +190,9 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
 #pragma unroll
         for (int k = 0; k < W; k++) {
           const int at = e + SPAN * k;
-          if (G) {
+          if (GROUPED) {
             f = e4m3_factor(__uint_as_float(gm[k]) * inv, s);
-            if (at < H && at % G == 0) scale[at / G] = s;
+            if (at < H && (at & (G - 1)) == 0) scale[at >> a.gshift] = s;
           }
           if (at >= H) continue;
           if (PER == 2) {
@@ -194,7 +209,8 @@ __global__ void __launch_bounds__(PACKS <= 2 ? 1024 : 512) rmsnorm_e4m3_kernel(c
 
 template <typename T, int PACKS, int A>
 static cudaError_t launch_norm_p(const NormArgs &a, dim3 block, cudaStream_t st) {
-  auto *k = rmsnorm_e4m3_kernel<T, PACKS, A>;
+  auto *k = a.group ? rmsnorm_e4m3_kernel<T, PACKS, A, true>
+                    : rmsnorm_e4m3_kernel<T, PACKS, A, false>;
   const int rows = (a.T + block.y - 1) / block.y;
   const int fit = std::max(1, cached_blocks_per_sm((const void *)k, block.x * block.y, 0));
   return launch_pdl(k, dim3(std::min(rows, fit * dev_info().sms)), block, 0, st, a);
@@ -215,9 +231,10 @@ static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
   // 63: fewer leave fewer loads in flight, more take the registers of other rows; fp32, twice
   // the bytes a pack: one 104 us, two 111).
   const bool one = a.T <= 2 * dev_info().sms || sizeof(T) == 4;
-  if (one && threads(1) <= 1024) return launch_norm_p<T, 1, A>(a, dim3(threads(1)), st);
-  if (threads(2) <= (one ? 1024 : 512)) return launch_norm_p<T, 2, A>(a, dim3(threads(2)), st);
-  if (threads(4) <= 512) return launch_norm_p<T, 4, A>(a, dim3(threads(4)), st);
+  auto fits = [&](int p) { return threads(p) <= norm_threads(p, sizeof(T)); };
+  if (one && fits(1)) return launch_norm_p<T, 1, A>(a, dim3(threads(1)), st);
+  if (fits(2)) return launch_norm_p<T, 2, A>(a, dim3(threads(2)), st);
+  if (fits(4)) return launch_norm_p<T, 4, A>(a, dim3(threads(4)), st);
   return launch_norm_p<T, 8, A>(a, dim3(threads(8)), st);
 }
 
@@ -255,8 +272,10 @@ extern "C" int moe_rmsnorm_e4m3(int T, int H, const void *x, long ldx, moe_dtype
   if ((uintptr_t)x % es || (uintptr_t)add % es || (uintptr_t)weight % es ||
       (uintptr_t)resid % es || (uintptr_t)scale % 4)
     return MOE_ERR_INVALID_ARG;
+  int gshift = 0;
+  while ((1 << gshift) < group) gshift++;
   const moe::NormArgs a{x, add, weight, resid, q, scale, ldx, add ? ldadd : 0, resid ? ldr : 0,
-                        ldq, T, H, group, normalize, eps};
+                        ldq, T, H, group, gshift, normalize, eps};
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = dtype == MOE_DT_F32    ? moe::launch_norm_t<float>(a, st)
                         : dtype == MOE_DT_BF16 ? moe::launch_norm_t<__nv_bfloat16>(a, st)
