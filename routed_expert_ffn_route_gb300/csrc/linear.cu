@@ -233,7 +233,7 @@ __device__ __forceinline__ float lin_act(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
     case MOE_ACT_SILU: return lin_silu<TO>(z);
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case MOE_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);  // z Phi(z)
     default: return z;
   }
 }
@@ -707,8 +707,11 @@ static int lin_clusters(int split) {
   attr[0].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) != cudaSuccess)
+  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) !=
+      cudaSuccess) {
+    cudaGetLastError();  // not an error of the call: the plan does without clusters
     n = 0;
+  }
   n = std::max(1, n);
   k.store(n, std::memory_order_relaxed);
   return n;

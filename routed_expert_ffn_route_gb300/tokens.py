@@ -17,13 +17,26 @@ import torch
 
 from . import MOE_DT_BF16, MOE_DT_E4M3, MOE_DT_F16, MOE_DT_F32, MOE_OK, MoEError, lib
 
-lib()  # raises if the library has not been built; the extension module is built with it
-from . import _tokens_native as _native  # noqa: E402
+
+class _Late:
+    """Stands for the extension module until the first call, which raises if the library has not
+    been built (the two are built together)."""
+
+    def __getattr__(self, name):
+        global _native
+        lib()
+        from . import _tokens_native
+        _native = _tokens_native
+        return getattr(_native, name)
+
+
+_native = _Late()
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 _F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
 _DTYPES = {_F32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16,
            _E4M3: MOE_DT_E4M3}
+
 
 def _row_type(dtype) -> int:
     t = _DTYPES.get(dtype)

@@ -291,6 +291,30 @@ def test_gradients_against_differences():
     assert abs(float((xs.double() * g).sum() - (dx.double() * x).sum())) < tol
 
 
+@pytest.mark.parametrize("H,dtype", [(8, TB), (9, TB), (64, T32)])
+def test_most_tokens_and_slots(H, dtype):
+    """65535 tokens with 16 slots each: rows out and back with weights of 1/16 are the tokens."""
+    T, k, E = 65535, 16, 256
+    off, perm, pos = sort_gpu(make_ids(8, T, k, E), E)
+    x = randn(1, T, H).to(dtype)
+    xs = torch.empty(T * k, H, dtype=dtype, device="cuda")
+    moe.moe_dispatch_rows(x, pos, off, xs)
+    out = torch.empty_like(x)
+    moe.moe_combine_rows(xs, pos, out, w=torch.full((T, k), 1 / 16, device="cuda"))
+    # sixteen equal terms: with 8 bits of significand every partial sum is exact in fp32; a term
+    # of 24 bits is not (three of them need 26), and each of its sums rounds once
+    few = torch.finfo(dtype).eps > 2 ** -20
+    within(out, x.double(), 0 if few else k * U * x.double().abs(), "back")
+    dx = torch.empty_like(x)
+    moe.moe_dispatch_rows_grad(xs, pos, dx)
+    within(dx, 16 * x.double(), 0 if few else k * U * 16 * x.double().abs(), "dx")
+    dy, dw = torch.empty_like(xs), torch.empty(T, k, device="cuda")
+    moe.moe_combine_rows_grad(x, xs, pos, off, None, dy, dw)
+    assert torch.equal(dy, xs)
+    sq = (x.double() ** 2).sum(1, keepdim=True)
+    within(dw, sq.expand(T, k), (8 + 16) * U * sq, "dw")
+
+
 # ------------------------------------------------------------------------------ linear
 def rows8(v):
     s = v.abs().amax(-1) / 448
@@ -412,6 +436,12 @@ def test_linear_types_and_activations(dt, od, act, bias, residual):
                                      (3000, 1040, 1024, 8)])
 def test_linear_by_expert(R, N, K, E, dt, act):
     run_linear(R, N, K, E, dt, TB, act, True, False, seed=R)
+
+
+@pytest.mark.parametrize("R,N,K,E", [(300000, 64, 64, 0), (200003, 48, 80, 3), (5, 40000, 64, 0),
+                                     (70, 20000, 48, 2)])
+def test_linear_many_rows_or_features(R, N, K, E):
+    run_linear(R, N, K, E, F8, TB, "none", True, False, seed=3)
 
 
 @pytest.mark.parametrize("counts", [[0, 0, 5, 0], [256, 0, 0, 1], [255, 1, 257, 0], [0, 0, 0, 0],
