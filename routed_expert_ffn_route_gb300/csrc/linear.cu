@@ -904,7 +904,9 @@ struct LinPlan {
 // of 128 rows), its loads (2.45 cycles a 128-byte row, 52 bytes a cycle into an SM) or 430
 // cycles, whichever is longest; joining a split tile takes 2000 cycles and 12 a column and
 // other CTA.  One token of 6144 x 2048 bf16: split 8 6.8 us, 4 9.4, 2 15.0, none 24.9; 200
-// tokens of 4096 x 4096: 112 columns split 2 13.4 us, 208 split 4 15.0, 64 unsplit 18.8.
+// tokens of 4096 x 4096: 112 columns split 2 13.4 us, 208 split 4 15.0, 64 unsplit 18.8.  Over 40
+// random shapes (1 to 20000 rows, 64 to 8192 features, K 128 to 14336, 0 to 64 experts) the form
+// taken is 3% slower than the fastest of all candidates in the mean, 26% at worst.
 static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
   const int sms = dev_info().sms;
   // experts that get rows, and rows of one of them, when rows fall on experts evenly
