@@ -6,7 +6,8 @@
 // The statistics are fp32.  The largest |y| of a group is the largest |r w| times the row's
 // factor, so the sum of squares and the maxima come out of the same single reduction and
 // every element is read from memory once: the row stays in registers between the reduction
-// and the encoding.
+// and the encoding.  Bound by memory: 8192 x 6144 bf16 with a residual moves 352 MB in 55 us, 6.4
+// TB/s of the 6.75 that a copy reaches.
 #include <cuda_fp8.h>
 
 #include <algorithm>
