@@ -438,6 +438,22 @@ def test_linear_by_expert(R, N, K, E, dt, act):
     run_linear(R, N, K, E, dt, TB, act, True, False, seed=R)
 
 
+# sizes at which pairs of CTAs share a tile (the first five) and clusters split K (the others)
+@pytest.mark.parametrize("R,N,K,E", [(2100, 1001, 1000, 0), (5000, 1001, 2048, 0),
+                                     (6000, 1501, 1024, 0), (2000, 300, 1024, 5),
+                                     (3000, 1040, 2000, 8), (257, 1000, 2048, 0),
+                                     (130, 700, 3840, 0), (40, 256, 1024, 16),
+                                     (256, 128, 4096, 0)])
+@pytest.mark.parametrize("od,act,bias,residual", [(TB, "none", True, True), (T32, "silu", True, False),
+                                                  (TH, "gelu", False, False),
+                                                  (T32, "swiglu", True, True),
+                                                  (TB, "swiglu", True, False)])
+def test_linear_pairs_and_splits(R, N, K, E, od, act, bias, residual):
+    N, K = (N - N % 16 if act == "swiglu" else N), K // 16 * 16
+    run_linear(R, N, K, E, F8, od, act, bias, residual, seed=R, pad=5)
+    run_linear(R, N, K // 32 * 16, E, TB, od, act, bias, residual, seed=R)
+
+
 @pytest.mark.parametrize("R,N,K,E", [(300000, 64, 64, 0), (200003, 48, 80, 3), (5, 40000, 64, 0),
                                      (70, 20000, 48, 2)])
 def test_linear_many_rows_or_features(R, N, K, E):
