@@ -1,6 +1,7 @@
 """Build the CUDA library in-tree: every csrc/*.cu compiled for sm_103a in parallel, then
 linked into libmoe_gb300.so next to this file, and the token operators' Python entry points
-(csrc/tokens_py.c).  No cmake; nvcc and a host compiler only."""
+(csrc/tokens_py.cpp, which reads tensors through torch's headers).  No cmake; nvcc and a C++
+host compiler only."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -58,7 +59,8 @@ def build(force: bool = False, extra=()) -> str:
         for o in glob.glob(os.path.join(OUT_DIR, "*.o")):
             os.remove(o)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        entries = ex.submit(_entries_obj, force)
         objs = list(ex.map(lambda s: _compile(s, list(extra)), srcs))
     if (not os.path.exists(LIB) or force or extra
             or max(os.path.getmtime(o) for o in objs) > os.path.getmtime(LIB)):
@@ -68,25 +70,48 @@ def build(force: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
-    _python_entries(force)
+    _link_entries(entries.result(), force)
     return LIB
 
 
-def _python_entries(force: bool):
-    """The token operators' CPython entry points, linked against the library beside them."""
-    src = os.path.join(CSRC, "tokens_py.c")
-    dep = max(os.path.getmtime(p) for p in [src, LIB] + _headers())
-    if os.path.exists(PY_EXT) and os.path.getmtime(PY_EXT) >= dep and not force:
-        return
-    tmp = PY_EXT + f".tmp{os.getpid()}"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-Wno-missing-field-initializers",
-           "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-o", tmp, src, "-L", HERE,
-           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+def _entries_obj(force: bool) -> str:
+    """Compile the token operators' Python entry points (torch's headers, a host compiler)."""
+    src = os.path.join(CSRC, "tokens_py.cpp")
+    obj = os.path.join(OUT_DIR, "tokens_py.o")
+    dep = max(os.path.getmtime(p) for p in [src] + _headers())
+    if os.path.exists(obj) and os.path.getmtime(obj) >= dep and not force:
+        return obj
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    abi = int(torch.compiled_with_cxx11_abi())
+    inc = [base, os.path.join(base, "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *(a for i in inc for a in ("-isystem", i)),
+           "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for tokens_py.c:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for tokens_py.cpp:\n{r.stderr}")
     if r.stderr.strip():
         sys.stderr.write(r.stderr)
+    return obj
+
+
+def _link_entries(obj: str, force: bool):
+    """The extension module beside the library it calls; torch's libraries are loaded by torch."""
+    if (os.path.exists(PY_EXT) and not force
+            and os.path.getmtime(PY_EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
+        return
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = PY_EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE,
+           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed for tokens_py.cpp:\n{r.stderr}")
     os.replace(tmp, PY_EXT)
 
 

@@ -1,0 +1,348 @@
+// tokens_py.cpp -- the token operators' entry points for Python.
+//
+// The package's other functions go through ctypes.  A call of a token operator has up to six
+// tensors and twenty arguments; reading the tensors from Python and converting the arguments with
+// ctypes took 5 us, twice the launch, and at decode sizes that is most of the call (7.3 us for a
+// norm of one row, 2.7 this way).  These
+// functions read the tensors through torch's C++ headers, check them, and call the C entry point
+// on the current stream of the operands' device, with the interpreter's lock released.  They
+// return its status; wrong shapes and strides raise ValueError, wrong types TypeError.  They
+// are private: tokens.py documents them.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <c10/cuda/CUDAStream.h>
+
+#include <exception>
+#include <initializer_list>
+#include <string>
+
+#include "../../include/moe.h"
+
+namespace {
+
+struct Raised {};  // a Python exception is set
+
+[[noreturn]] void raise(PyObject *type, const std::string &text) {
+  PyErr_SetString(type, text.c_str());
+  throw Raised{};
+}
+
+const at::Tensor &tensor(PyObject *o, const char *name) {
+  if (!THPVariable_Check(o)) raise(PyExc_TypeError, std::string(name) + " must be a tensor");
+  return THPVariable_Unpack(o);
+}
+
+int row_type(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return MOE_DT_F32;
+    case at::kBFloat16: return MOE_DT_BF16;
+    case at::kHalf: return MOE_DT_F16;
+    case at::kFloat8_e4m3fn: return MOE_DT_E4M3;
+    default:
+      raise(PyExc_TypeError, "rows must be float32, bfloat16, float16 or float8_e4m3fn, got " +
+                                 std::string(c10::toString(t)));
+  }
+}
+
+std::string text(std::initializer_list<int64_t> shape) {
+  std::string s = "[";
+  for (int64_t v : shape) s += (s.size() > 1 ? ", " : "") + std::to_string(v);
+  return s + "]";
+}
+
+// a 32-bit size of the C interface
+int size32(int64_t v, const char *name) {
+  if (v > 2147483647) raise(PyExc_ValueError, std::string(name) + " is too large");
+  return (int)v;
+}
+
+// The operands of one call: all on one CUDA device.
+struct Call {
+  int dev;
+  explicit Call(const at::Tensor &first) : dev(first.is_cuda() ? first.get_device() : -1) {}
+
+  void check(const at::Tensor &t, const char *name, at::ScalarType type,
+             std::initializer_list<int64_t> shape) const {
+    if (!t.sizes().equals(c10::IntArrayRef(shape.begin(), shape.size()))) {
+      std::string got = "[";
+      for (int64_t v : t.sizes()) got += (got.size() > 1 ? ", " : "") + std::to_string(v);
+      raise(PyExc_ValueError,
+            std::string(name) + " must have shape " + text(shape) + ", got " + got + "]");
+    }
+    if (t.scalar_type() != type)
+      raise(PyExc_TypeError, std::string(name) + " must be " + c10::toString(type) + ", got " +
+                                 c10::toString(t.scalar_type()));
+    if ((t.is_cuda() ? t.get_device() : -1) != dev)
+      raise(PyExc_ValueError, std::string(name) + " is on another device than the first operand");
+  }
+  // rows that may lie apart: the address, and the distance between rows
+  void *rows(PyObject *o, const char *name, at::ScalarType type, int64_t n, int64_t width,
+             long &ld) const {
+    const at::Tensor &t = tensor(o, name);
+    check(t, name, type, {n, width});
+    ld = (long)t.stride(0);
+    if (width > 1 && t.stride(1) != 1)
+      raise(PyExc_ValueError, std::string(name) + "'s last dimension must be contiguous");
+    if (ld < width) {
+      if (n > 1) raise(PyExc_ValueError, std::string(name) + "'s rows overlap");
+      ld = (long)width;
+    }
+    return t.data_ptr();
+  }
+  void *rows_or_null(PyObject *o, const char *name, at::ScalarType type, int64_t n, int64_t width,
+                     long &ld) const {
+    ld = 0;
+    return o == Py_None ? nullptr : rows(o, name, type, n, width, ld);
+  }
+  void *flat(PyObject *o, const char *name, at::ScalarType type,
+             std::initializer_list<int64_t> shape) const {
+    const at::Tensor &t = tensor(o, name);
+    check(t, name, type, shape);
+    if (!t.is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be contiguous");
+    return t.data_ptr();
+  }
+  void *flat_or_null(PyObject *o, const char *name, at::ScalarType type,
+                     std::initializer_list<int64_t> shape) const {
+    return o == Py_None ? nullptr : flat(o, name, type, shape);
+  }
+  // the given stream's handle, or the current stream of the operands' device
+  void *stream(PyObject *o) const {
+    if (dev < 0) raise(PyExc_ValueError, "operands must be on a CUDA device");
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+    void *s = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Raised{};
+    return s;
+  }
+};
+
+int64_t dim(const at::Tensor &t, const char *name, int dims, int i) {
+  if (t.dim() != dims)
+    raise(PyExc_ValueError, std::string(name) + " must have " + std::to_string(dims) +
+                                " dimensions, got " + std::to_string(t.dim()));
+  return t.size(i);
+}
+
+long number(PyObject *o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+int number32(PyObject *o, const char *name) { return size32(number(o), name); }
+
+// Runs a function that returns a status; C++ exceptions become Python's.
+template <typename F>
+PyObject *run(Py_ssize_t n, Py_ssize_t want, F body) {
+  try {
+    if (n != want) raise(PyExc_TypeError, "wrong number of arguments");
+    return PyLong_FromLong(body());
+  } catch (const Raised &) {
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+// the interpreter's lock, released for a scope
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// x, q, scale, add, weight, resid, eps, group, normalize, stream
+PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 10, [&]() {
+    const at::Tensor &x = tensor(a[0], "x");
+    const Call c(x);
+    const int64_t T = dim(x, "x", 2, 0), H = x.size(1);
+    const at::ScalarType dt = x.scalar_type();
+    const int group = number32(a[7], "group"), normalize = PyObject_IsTrue(a[8]);
+    const float eps = (float)PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) throw Raised{};
+    long ldx, ldq, lda, ldr;
+    const void *px = c.rows(a[0], "x", dt, T, H, ldx);
+    uint8_t *pq = (uint8_t *)c.rows(a[1], "q", at::kFloat8_e4m3fn, T, H, ldq);
+    float *ps = (float *)c.flat(a[2], "scale", at::kFloat,
+                                {T, group > 0 ? (H + group - 1) / group : 1});
+    const void *pa = c.rows_or_null(a[3], "add", dt, T, H, lda);
+    const void *pw = c.flat_or_null(a[4], "weight", dt, {H});
+    void *pr = c.rows_or_null(a[5], "resid", dt, T, H, ldr);
+    const int rt = row_type(dt);
+    const int t32 = size32(T, "x"), h32 = size32(H, "x");
+    void *st = c.stream(a[9]);
+    const Unlocked unlocked;
+    return moe_rmsnorm_e4m3(t32, h32, px, ldx, (moe_dtype)rt, pa, lda, pw, eps, normalize,
+                            group, pr, ldr, pq, ldq, ps, st);
+  });
+}
+
+// ids, n_experts, offsets, perm, slot_pos, stream
+PyObject *sort(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 6, [&]() {
+    const at::Tensor &ids = tensor(a[0], "ids");
+    const Call c(ids);
+    const int64_t T = dim(ids, "ids", 2, 0), k = ids.size(1), E = number(a[1]);
+    const int32_t *pi = (const int32_t *)c.flat(a[0], "ids", at::kInt, {T, k});
+    int32_t *po = (int32_t *)c.flat(a[2], "offsets", at::kInt, {E + 1});
+    int32_t *pp = (int32_t *)c.flat(a[3], "perm", at::kInt, {T * k});
+    int32_t *ps = (int32_t *)c.flat(a[4], "slot_pos", at::kInt, {T, k});
+    const int t32 = size32(T, "ids"), k32 = size32(k, "ids"), e32 = size32(E, "n_experts");
+    void *st = c.stream(a[5]);
+    const Unlocked unlocked;
+    return moe_sort_tokens(t32, k32, e32, pi, po, pp, ps, st);
+  });
+}
+
+// x, slot_pos, offsets, xs, scale, scale_s, stream
+PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 7, [&]() {
+    const at::Tensor &x = tensor(a[0], "x");
+    const Call c(x);
+    const int64_t T = dim(x, "x", 2, 0), H = x.size(1);
+    const int64_t k = dim(tensor(a[1], "slot_pos"), "slot_pos", 2, 1);
+    const int64_t E1 = dim(tensor(a[2], "offsets"), "offsets", 1, 0);
+    const at::ScalarType dt = x.scalar_type();
+    long ldx, ldsc = 0;
+    const void *px = c.rows(a[0], "x", dt, T, H, ldx);
+    const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
+    const int32_t *po = (const int32_t *)c.flat(a[2], "offsets", at::kInt, {E1});
+    void *pxs = c.flat(a[3], "xs", dt, {T * k, H});
+    int64_t S = 0;
+    const float *psc = nullptr;
+    float *pss = nullptr;
+    if (a[4] != Py_None) {
+      S = dim(tensor(a[4], "scale"), "scale", 2, 1);
+      psc = (const float *)c.rows(a[4], "scale", at::kFloat, T, S, ldsc);
+      if (a[5] == Py_None) raise(PyExc_ValueError, "scale_s is needed with scale");
+      pss = (float *)c.flat(a[5], "scale_s", at::kFloat, {T * k, S});
+    }
+    const int rt = row_type(dt), t32 = size32(T, "x"), k32 = size32(k, "slot_pos");
+    const int h32 = size32(H, "x"), s32 = size32(S, "scale"), e32 = size32(E1 - 1, "offsets");
+    void *st = c.stream(a[6]);
+    const Unlocked unlocked;
+    return moe_dispatch_rows(t32, k32, e32, h32, (moe_dtype)rt, px, ldx, pp, po, pxs, s32, psc,
+                             ldsc, pss, st);
+  });
+}
+
+// y, slot_pos, out, w, add, stream
+PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 6, [&]() {
+    const at::Tensor &y = tensor(a[0], "y"), &pos = tensor(a[1], "slot_pos");
+    const at::Tensor &out = tensor(a[2], "out");
+    const Call c(y);
+    const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(out, "out", 2, 1);
+    const at::ScalarType yt = y.scalar_type(), ot = out.scalar_type();
+    long ldo, lda;
+    const void *py = c.flat(a[0], "y", yt, {T * k, H});
+    const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
+    void *po = c.rows(a[2], "out", ot, T, H, ldo);
+    const float *pw = (const float *)c.flat_or_null(a[3], "w", at::kFloat, {T, k});
+    const void *pa = c.rows_or_null(a[4], "add", ot, T, H, lda);
+    const int ry = row_type(yt), ro = row_type(ot), t32 = size32(T, "slot_pos");
+    const int k32 = size32(k, "slot_pos"), h32 = size32(H, "out");
+    void *st = c.stream(a[5]);
+    const Unlocked unlocked;
+    return moe_combine_rows(t32, k32, h32, py, (moe_dtype)ry, pp, pw, pa, lda, po, ldo,
+                            (moe_dtype)ro, st);
+  });
+}
+
+// dout, y, slot_pos, offsets, w, dy, dw, stream
+PyObject *combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 8, [&]() {
+    const at::Tensor &dout = tensor(a[0], "dout"), &pos = tensor(a[2], "slot_pos");
+    const Call c(dout);
+    const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(dout, "dout", 2, 1);
+    const int64_t E1 = dim(tensor(a[3], "offsets"), "offsets", 1, 0);
+    const at::ScalarType dt = dout.scalar_type();
+    long ldd;
+    const void *pd = c.rows(a[0], "dout", dt, T, H, ldd);
+    const void *py = c.flat(a[1], "y", dt, {T * k, H});
+    const int32_t *pp = (const int32_t *)c.flat(a[2], "slot_pos", at::kInt, {T, k});
+    const int32_t *po = (const int32_t *)c.flat(a[3], "offsets", at::kInt, {E1});
+    const float *pw = (const float *)c.flat_or_null(a[4], "w", at::kFloat, {T, k});
+    void *pdy = c.flat(a[5], "dy", dt, {T * k, H});
+    float *pdw = (float *)c.flat(a[6], "dw", at::kFloat, {T, k});
+    const int rt = row_type(dt), t32 = size32(T, "slot_pos"), k32 = size32(k, "slot_pos");
+    const int h32 = size32(H, "dout"), e32 = size32(E1 - 1, "offsets");
+    void *st = c.stream(a[7]);
+    const Unlocked unlocked;
+    return moe_combine_rows_grad(t32, k32, e32, h32, (moe_dtype)rt, pd, ldd, py, pp, po, pw, pdy,
+                                 pdw, st);
+  });
+}
+
+// dxs, slot_pos, dx, stream
+PyObject *dispatch_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 4, [&]() {
+    const at::Tensor &dxs = tensor(a[0], "dxs"), &pos = tensor(a[1], "slot_pos");
+    const at::Tensor &dx = tensor(a[2], "dx");
+    const Call c(dxs);
+    const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(dx, "dx", 2, 1);
+    const at::ScalarType dt = dxs.scalar_type(), xt = dx.scalar_type();
+    long ldx;
+    const void *pd = c.flat(a[0], "dxs", dt, {T * k, H});
+    const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
+    void *px = c.rows(a[2], "dx", xt, T, H, ldx);
+    const int rd = row_type(dt), rx = row_type(xt), t32 = size32(T, "slot_pos");
+    const int k32 = size32(k, "slot_pos"), h32 = size32(H, "dx");
+    void *st = c.stream(a[3]);
+    const Unlocked unlocked;
+    return moe_dispatch_rows_grad(t32, k32, h32, (moe_dtype)rd, pd, pp, px, ldx, (moe_dtype)rx,
+                                  st);
+  });
+}
+
+// x, w, out, x_scale, w_scale, bias, act, residual, offsets, status, stream
+PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return run(n, 11, [&]() {
+    const at::Tensor &x = tensor(a[0], "x"), &out = tensor(a[2], "out");
+    const Call c(x);
+    const int64_t R = dim(x, "x", 2, 0), K = x.size(1), N = dim(out, "out", 2, 1);
+    const at::ScalarType dt = x.scalar_type(), ot = out.scalar_type();
+    const int act = number32(a[6], "act");
+    const int64_t rows = act == MOE_ACT_SWIGLU ? 2 * N : N;
+    const bool dense = a[8] == Py_None;
+    int64_t E = 0;
+    const int32_t *po = nullptr;
+    if (!dense) {
+      E = dim(tensor(a[8], "offsets"), "offsets", 1, 0) - 1;
+      if (E < 1) raise(PyExc_ValueError, "offsets must hold E + 1 values");
+      po = (const int32_t *)c.flat(a[8], "offsets", at::kInt, {E + 1});
+    }
+    long ldx, ldo, ldr;
+    const void *px = c.rows(a[0], "x", dt, R, K, ldx);
+    const void *pw = dense ? c.flat(a[1], "w", dt, {rows, K}) : c.flat(a[1], "w", dt, {E, rows, K});
+    void *pout = c.rows(a[2], "out", ot, R, N, ldo);
+    const float *pxs = nullptr;
+    if (a[3] != Py_None)
+      pxs = (const float *)(tensor(a[3], "x_scale").dim() == 1
+                                ? c.flat(a[3], "x_scale", at::kFloat, {R})
+                                : c.flat(a[3], "x_scale", at::kFloat, {R, 1}));
+    auto per_row = [&](PyObject *o, const char *name) {
+      return (const float *)(dense ? c.flat_or_null(o, name, at::kFloat, {rows})
+                                   : c.flat_or_null(o, name, at::kFloat, {E, rows}));
+    };
+    const float *pws = per_row(a[4], "w_scale"), *pb = per_row(a[5], "bias");
+    const void *pr = c.rows_or_null(a[7], "residual", ot, R, N, ldr);
+    int32_t *pst = (int32_t *)c.flat_or_null(a[9], "status", at::kInt, {1});
+    const int rt = row_type(dt), ro = row_type(ot), r32 = size32(R, "x"), n32 = size32(N, "out");
+    const int k32 = size32(K, "x"), e32 = size32(E, "offsets");
+    void *st = c.stream(a[10]);
+    const Unlocked unlocked;
+    return moe_linear(r32, n32, k32, e32, px, ldx, (moe_dtype)rt, pxs, pw, pws, pb, (moe_act)act,
+                      pr, ldr, po, pout, ldo, (moe_dtype)ro, pst, st);
+  });
+}
+
+#define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {METHOD(rmsnorm),      METHOD(sort),          METHOD(dispatch),
+                         METHOD(combine),      METHOD(combine_grad),  METHOD(dispatch_grad),
+                         METHOD(linear),       {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens_native", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tokens_native(void) { return PyModule_Create(&module); }
