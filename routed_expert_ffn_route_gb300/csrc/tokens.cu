@@ -25,16 +25,17 @@ namespace moe {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxE = 256;
-constexpr int kSortCluster = 8;
 
-// A stable counting sort in one launch: one CTA, or a cluster of eight for long id arrays.
+
+// A stable counting sort in one launch: one CTA, or a cluster of eight or sixteen for long id
+// arrays.
 // Each warp owns a contiguous run of slots and counts it into its own row of `hist`; the rows
 // are scanned over the warps, the CTA totals over the cluster (distributed shared memory), the
 // expert totals over the experts; then each warp walks its run again, 32 slots at a time, and
 // gives a slot the position base + expert's slots so far + equal ids in lower lanes.  The lanes
 // of an id come from a mask in shared memory that every lane sets its bit in (the order of those
 // atomics does not matter); match_any finds them too, but slower: 65,536 slots of 256 experts
-// 21 us against 10.
+// 21 us against 10 on eight CTAs.
 struct SortShared {
   int hist[kSortWarps][kSortMaxE];       // slots of the warp's run, then positions handed out
   uint32_t mask[kSortWarps][kSortMaxE];  // the lanes of each id among the warp's 32 slots
@@ -470,8 +471,14 @@ int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *of
   if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)perm | (uintptr_t)slot_pos) % 4)
     return MOE_ERR_INVALID_ARG;
   const int n = T * k;
-  // a warp walks its run 32 slots at a time: past two steps a warp, eight CTAs
-  const int ctas = n <= kSortThreads * 2 ? 1 : kSortCluster;
+  // a warp walks its run 32 slots at a time: past two steps a warp, eight CTAs; past four steps
+  // of those, sixteen (65,536 slots: 10.0 us with eight, 8.4 with sixteen;
+  // 262,144: 27.9 and 17.7)
+  const int ctas = n <= kSortThreads * 2 ? 1 : n <= kSortThreads * 32 ? 8 : 16;
+  if (ctas == 16 && cudaFuncSetAttribute(sort_tokens_kernel,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                        cudaSuccess)
+    return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   // one CTA: a warp for every 32 slots (in eights, as the scan takes them), and the scans' threads

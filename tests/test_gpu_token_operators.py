@@ -511,6 +511,23 @@ def test_linear_large_offsets_in_weights():
     within(out, ref, err + U * ref.abs(), "last expert")
 
 
+def test_refusals_raise_the_status():
+    """What the C entry points refuse reaches Python as MoEError with the status."""
+    ids = torch.zeros(3, 17, dtype=torch.int32, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    perm = torch.zeros(51, dtype=torch.int32, device="cuda")
+    x, q = randn(1, 4, 72, dtype=TB), torch.empty(4, 72, dtype=F8, device="cuda")
+    calls = [lambda: moe.moe_sort_tokens(ids, 4, off, perm, ids),
+             lambda: moe.moe_rmsnorm_e4m3(x, q, torch.empty(4, 5, device="cuda"), group=16),
+             lambda: moe.moe_linear(x, randn(2, 8, 72, dtype=TB), torch.empty(4, 8, device="cuda"))]
+    for f in calls:
+        with pytest.raises(moe.MoEError) as e:
+            f()
+        assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):  # an operand on the host
+        moe.moe_rmsnorm_e4m3(x, q, torch.empty(4, 1))
+
+
 # ------------------------------------------------------------------ together, captured
 def test_chain_repeats_bit_for_bit_on_a_stream_and_in_a_graph():
     """Norm -> sort -> rows out -> gate/up -> quantise -> down -> back, eagerly on a side
