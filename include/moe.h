@@ -360,7 +360,8 @@ int moe_dispatch_rows_grad(int T, int k, int H, moe_dtype dtype, const void *dxs
  * moe_sort_tokens writes it; values are clamped to [0, R] and to ascending order); rows of no
  * expert get zeros and are not read.  act = SWIGLU: w has 2 N rows per expert (gate rows, then
  * up rows; w_scale and bias too) and out = silu(z_gate) * z_up + residual.
- * Accumulation is fp32 on the tensor cores.  x, w and x's rows 16-byte aligned; K a multiple
+ * Accumulation is fp32 on the tensor cores, whose sums are truncated; for F32 outputs they are
+ * added up in registers every few hundred of K, rounded to nearest.  x, w and x's rows 16-byte aligned; K a multiple
  * of 16, N of 16 for SWIGLU, E <= 256, else MOE_ERR_UNSUPPORTED.  status: optional device
  * int32, set to MOE_ERR_TIMEOUT if a bounded wait gave up (the output is then undefined), else
  * left as it is. */

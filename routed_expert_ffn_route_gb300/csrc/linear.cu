@@ -47,6 +47,20 @@ constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk
 constexpr int kLinStage = kLinEpi * 16 * kLinPitch * 4;  // bytes of the staged chunks
 constexpr long kLinWaitNs = 2000000000L;
 
+// fp32 outputs: the tensor cores truncate each sum to fp32 (K = 6144 bf16 loses 6e-6 of the result
+// that way, 1.4e-5 of a SwiGLU's), so they sum kLinExact k-blocks at a time and the epilogue warps
+// add those sums, rounded to nearest, in registers: 3e-7 and 5e-7.  (4096^3 bf16 takes 152 us so;
+// eight k-blocks 134, with twice the error; the two accumulators of a pair wait on each other
+// across its CTAs and take 179.)  16-bit outputs, rounded to 2^-9 or 2^-12, are summed to the end in
+// tensor memory.
+constexpr int kLinExact = 4;
+template <typename TO>
+constexpr bool lin_exact = sizeof(TO) == 4;
+// columns between the two accumulators, and the largest tiles whose sums fit the registers
+template <typename TO>
+constexpr int kLinAcc = lin_exact<TO> ? 128 : kLinMaxN;
+constexpr int kLinExactN = 128, kLinExactSplitN = 64;
+
 // How CTAs share a tile:
 //   kOne    one CTA a tile, persistent.
 //   kPair   two CTAs (the two SMs of a TPC) a tile of 256 weight rows: each loads its own 128
@@ -341,6 +355,21 @@ struct LinOut {
     __syncwarp();
   }
 
+  // the same of sums that are in registers
+  template <int NI>
+  __device__ __forceinline__ void tile_sums(const float (&sum)[NI][16], int n, int half, int lane,
+                                            const float *xs) const {
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+      const int c0 = 16 * half + 32 * i;
+      if (c0 < n) {
+        Pack<TO> rv[IT];
+        prefetch(c0, n, lane, rv);
+        finish(c0, n, lane, xs + 16 * i, sum[i], rv);
+      }
+    }
+  }
+
   // the warp's chunks of a tile of n columns: the even (half = 0) or the odd ones
   __device__ __forceinline__ void tile(uint32_t taddr, int n, int half, int lane,
                                        const float *xs) const {
@@ -499,13 +528,49 @@ struct LinOut16 {
   }
 };
 
+// fp32 outputs: this warp's chunks of 16 columns (every second one of a tile's, NI of them at
+// most), summed over the accumulators of a tile's k-blocks; false when a wait gave up
+template <int NI, int ACC>
+__device__ __forceinline__ bool lin_sum(LinBars *b, uint32_t taddr, int n, int half, int lane,
+                                        int kblocks, int &buf, uint32_t &bph, float (&sum)[NI][16],
+                                        volatile int *abort) {
+#pragma unroll
+  for (int i = 0; i < NI; i++)
+#pragma unroll
+    for (int j = 0; j < 16; j++) sum[i][j] = 0.f;
+  for (int k0 = 0; k0 < kblocks; k0 += kLinExact) {
+    if (!__all_sync(0xffffffffu,
+                    tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 32)))
+      return false;
+    tc::fence_after_sync();
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+      const int c0 = 16 * half + 32 * i;
+      if (c0 < n) {
+        uint32_t v[16];
+        __syncwarp();
+        tc::tmem_ld16(taddr + buf * ACC + c0, v);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j++) sum[i][j] += __uint_as_float(v[j]);
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&b->acc_empty[buf]);
+    if (buf) bph ^= 1;
+    buf ^= 1;
+  }
+  return true;
+}
+
 // LinOut16's output type (fp32 outputs take LinOut)
 template <typename TO>
 using H16 = std::conditional_t<sizeof(TO) == 2, TO, __half>;
 
 // The tiles of one epilogue warp.  The scales and biases of the next tile are loaded while this
 // one is worked on.
-template <typename OUT, bool PAIR>
+template <typename OUT, bool PAIR, bool EXACT>
 __device__ __forceinline__ void lin_epilogue(const LinArgs &a, LinBars *b, uint32_t tbase, int tile,
                                              int ctas, int total, uint32_t rank, int warp, int lane,
                                              float *stage, volatile int *abort) {
@@ -536,6 +601,14 @@ __device__ __forceinline__ void lin_epilogue(const LinArgs &a, LinBars *b, uint3
       t = lin_tile(a, b, tile + ctas);
       o = OUT(a, t, PAIR ? 2 * t.ft + rank : t.ft, quad, lane, stage);
       scales(t);
+    }
+    if constexpr (EXACT) {
+      float sum[kLinExactN / 32][16];
+      if (!lin_sum<kLinExactN / 32, kLinAcc<float>>(b, tbase + ((uint32_t)(32 * quad) << 16), n,
+                                                    half, lane, a.KB, buf, bph, sum, abort))
+        break;
+      now.tile_sums(sum, n, half, lane, xs);
+      continue;
     }
     if (!__all_sync(0xffffffffu,
                     tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
@@ -648,6 +721,7 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
   const int ctas = PAIR ? gridDim.x / 2 : SPLIT ? gridDim.x / a.split : gridDim.x;
   const int kb0 = SPLIT ? (int)((long)a.KB * rank / a.split) : 0;
   const int kb1 = SPLIT ? (int)((long)a.KB * (rank + 1) / a.split) : a.KB;
+  const int chunk = lin_exact<TO> ? kLinExact : kb1 - kb0;  // k-blocks summed in tensor memory
 
   if (warp == 0) {
     if (lane == 0) {
@@ -697,40 +771,42 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
       const LinTile t = lin_tile(a, b, tile);
       const uint32_t idesc = tc::idesc_f16(a.bf16, round16(t.n)) +
                              (PAIR ? (uint32_t)(kLinM >> 4) << 24 : 0u);  // M = 256
-      int got = 1;
-      if (leader) got = tc::mbar_wait(&b->acc_empty[buf], bph ^ 1, abort, kLinWaitNs);
-      ok = __all_sync(0xffffffffu, got);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t d = tbase + buf * kLinMaxN;
-      for (int kb = kb0; kb < kb1; kb++) {
-        if (leader) got = tc::mbar_wait_spin(&b->full[s], ph, abort, kLinWaitNs);
+      for (int k0 = kb0; k0 < kb1 && ok; k0 += chunk) {  // an accumulator each
+        int got = 1;
+        if (leader) got = tc::mbar_wait(&b->acc_empty[buf], bph ^ 1, abort, kLinWaitNs);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc::fence_after_sync();
-        if (leader) {
-          const uint32_t sa = tc::smem_u32(ring) + (uint32_t)(s * stage_bytes);
-          const uint64_t da = tc::sdesc_sw128(sa), db = tc::sdesc_sw128(sa + kLinM * 128);
-          if (a.kind8) {
+        const uint32_t d = tbase + buf * kLinAcc<TO>;
+        for (int kb = k0; kb < min(k0 + chunk, kb1); kb++) {
+          if (leader) got = tc::mbar_wait_spin(&b->full[s], ph, abort, kLinWaitNs);
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (leader) {
+            const uint32_t sa = tc::smem_u32(ring) + (uint32_t)(s * stage_bytes);
+            const uint64_t da = tc::sdesc_sw128(sa), db = tc::sdesc_sw128(sa + kLinM * 128);
+            if (a.kind8) {
 #pragma unroll
-            for (int kk = 0; kk < 4; kk++)
-              lin_mma<PAIR, true>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > kb0) | (kk != 0));
-          } else {
+              for (int kk = 0; kk < 4; kk++)
+                lin_mma<PAIR, true>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > k0) | (kk != 0));
+            } else {
 #pragma unroll
-            for (int kk = 0; kk < 4; kk++)
-              lin_mma<PAIR, false>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > kb0) | (kk != 0));
+              for (int kk = 0; kk < 4; kk++)
+                lin_mma<PAIR, false>(d, da + 2 * kk, db + 2 * kk, idesc, (kb > k0) | (kk != 0));
+            }
+            lin_commit<PAIR>(&b->empty[s]);
           }
-          lin_commit<PAIR>(&b->empty[s]);
+          __syncwarp();
+          issued = true;
+          if (++s == a.stages) s = 0, ph ^= 1;
         }
+        if (!ok) break;
+        if (leader) lin_commit<PAIR>(&b->acc_full[buf]);
         __syncwarp();
-        issued = true;
-        if (++s == a.stages) s = 0, ph ^= 1;
+        if (buf) bph ^= 1;
+        buf ^= 1;
       }
-      if (!ok) break;
-      if (leader) lin_commit<PAIR>(&b->acc_full[buf]);
-      __syncwarp();
-      if (buf) bph ^= 1;
-      buf ^= 1;
     }
     if (leader && !ok) {
       give_up();
@@ -741,11 +817,11 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
     }
   } else if (!SPLIT) {
     if (sizeof(TO) == 2 && !a.residual)
-      lin_epilogue<LinOut16<H16<TO>, GATED>, PAIR>(a, b, tbase, cta, ctas, total, rank, warp, lane,
-                                                   stage, abort);
+      lin_epilogue<LinOut16<H16<TO>, GATED>, PAIR, false>(a, b, tbase, cta, ctas, total, rank, warp,
+                                                          lane, stage, abort);
     else
-      lin_epilogue<LinOut<TO, GATED>, PAIR>(a, b, tbase, cta, ctas, total, rank, warp, lane, stage,
-                                            abort);
+      lin_epilogue<LinOut<TO, GATED>, PAIR, lin_exact<TO>>(a, b, tbase, cta, ctas, total, rank,
+                                                           warp, lane, stage, abort);
   }
   if (SPLIT) {
     // ---------------------------------------------------- a tile's partial sums, joined
@@ -762,28 +838,50 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
     LinTile t{};
     if (work) t = lin_tile(a, b, cta);
     const LinOut<TO, GATED> o(a, t, t.ft, quad, lane, stage);
+    const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16);
+    float sum[kLinExactSplitN / 32][16];  // fp32 outputs
     if (warp >= 2 && work) {
       for (int c = tid - 64; c < kLinMaxN; c += 32 * kLinEpi)
         xs[c] = c < t.n ? a.x_scale ? a.x_scale[t.r0 + c] : 1.f : 0.f;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_backoff(&b->acc_full[0], 0, abort, kLinWaitNs, 32));
-      tc::fence_after_sync();
+      if constexpr (lin_exact<TO>) {
+        int buf = 0;
+        uint32_t bph = 0;
+        ok = lin_sum<kLinExactSplitN / 32, kLinAcc<TO>>(b, taddr, t.n, half, lane, kb1 - kb0, buf,
+                                                       bph, sum, abort);
+      } else {
+        ok = __all_sync(0xffffffffu,
+                        tc::mbar_wait_backoff(&b->acc_full[0], 0, abort, kLinWaitNs, 32));
+        tc::fence_after_sync();
+      }
     }
     __syncwarp();
     cluster_wait();  // every CTA of the cluster has started: its memory may be written
-    if (warp >= 2 && ok) {
-      const uint32_t taddr = tbase + ((uint32_t)(32 * quad) << 16);
-      for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
-        uint32_t v[16];
-        __syncwarp();
-        tc::tmem_ld16(taddr + c0, v);
-        tc::tmem_wait_ld();
+    auto send = [&](int c0, const uint32_t (&v)[16]) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const uint32_t to = ((uint32_t)(c0 + j) * inv) >> 16;  // (c0 + j) / cpc
-          if (c0 + j < t.n)
-            store_in_cta(in_cta(ring + a.ring, to) +
-                             (rank * cpc + c0 + j - to * cpc) * (kLinM * 4) + row * 16,
-                         v + j);
+      for (int j = 0; j < 16; j += 4) {
+        const uint32_t to = ((uint32_t)(c0 + j) * inv) >> 16;  // (c0 + j) / cpc
+        if (c0 + j < t.n)
+          store_in_cta(in_cta(ring + a.ring, to) +
+                           (rank * cpc + c0 + j - to * cpc) * (kLinM * 4) + row * 16,
+                       v + j);
+      }
+    };
+    if (warp >= 2 && ok) {
+      if constexpr (lin_exact<TO>) {
+#pragma unroll
+        for (int i = 0; i < kLinExactSplitN / 32; i++) {
+          uint32_t v[16];
+#pragma unroll
+          for (int j = 0; j < 16; j++) v[j] = __float_as_uint(sum[i][j]);
+          send(16 * half + 32 * i, v);
+        }
+      } else {
+        for (int c0 = 16 * half; c0 < t.n; c0 += 32) {
+          uint32_t v[16];
+          __syncwarp();
+          tc::tmem_ld16(taddr + c0, v);
+          tc::tmem_wait_ld();
+          send(c0, v);
         }
       }
     }
@@ -911,7 +1009,7 @@ struct LinPlan {
 // tokens of 4096 x 4096: 112 columns split 2 13.4 us, 208 split 4 15.0, 64 unsplit 18.8.  Over 40
 // random shapes (1 to 20000 rows, 64 to 8192 features, K 128 to 14336, 0 to 64 experts) the form
 // taken is 3% slower than the fastest of all candidates in the mean, 26% at worst.
-static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
+static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated, bool exact) {
   const int sms = dev_info().sms;
   // experts that get rows, and rows of one of them, when rows fall on experts evenly
   const double active = E > 1 ? E * (1.0 - std::pow(1.0 - 1.0 / E, R)) : 1.0;
@@ -924,6 +1022,8 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
       for (int split = mode == kSplit ? 2 : 1; split <= (mode == kSplit ? 8 : 1); split *= 2) {
         if (mode == kPair && (BN < 64 || BN % 32 || rows <= kLinM)) continue;
         if (split > KB) continue;
+        if (exact && (mode == kPair || BN > (mode == kSplit ? kLinExactSplitN : kLinExactN)))
+          continue;
         const int FT = (rows + (mode == kPair ? 255 : 127)) / (mode == kPair ? 256 : 128);
         // row tiles of an expert: exact when dense; by expert the last one is about half full,
         // and experts differ in size
@@ -956,20 +1056,21 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated) {
 }
 
 // the plans of the last sizes seen by this thread (the estimate costs about a launch)
-static LinPlan lin_plan(int R, int N, int E, int KB, bool gated) {
+static LinPlan lin_plan(int R, int N, int E, int KB, bool gated, bool exact) {
   struct Entry {
-    int R, N, E, KB, gated, dev;
+    int R, N, E, KB, form, dev;
     LinPlan plan;
   };
   static thread_local Entry seen[64];
+  const int form = 2 * gated + exact;
   int dev = 0;
   cudaGetDevice(&dev);
   const uint32_t h = ((uint32_t)R * 2654435761u) ^ ((uint32_t)N * 2246822519u) ^
-                     ((uint32_t)KB * 3266489917u) ^ (uint32_t)(E * 2 + gated) * 668265263u;
+                     ((uint32_t)KB * 3266489917u) ^ (uint32_t)(E * 4 + form) * 668265263u;
   Entry &e = seen[(h >> 16) & 63];
-  if (e.R == R && e.N == N && e.E == E && e.KB == KB && e.gated == gated && e.dev == dev)
+  if (e.R == R && e.N == N && e.E == E && e.KB == KB && e.form == form && e.dev == dev)
     return e.plan;
-  e = Entry{R, N, E, KB, gated, dev, lin_make_plan(R, N, E, KB, gated)};
+  e = Entry{R, N, E, KB, form, dev, lin_make_plan(R, N, E, KB, gated, exact)};
   return e.plan;
 }
 
@@ -999,9 +1100,10 @@ static int launch_linear(const CUtensorMap &xm, const CUtensorMap &wm, const Lin
 template <typename TO, bool GATED>
 static int launch_linear_m(const CUtensorMap &xm, const CUtensorMap &wm, const LinArgs &a,
                            const LinPlan &p, cudaStream_t st) {
-  return p.mode == kPair    ? launch_linear<TO, GATED, kPair>(xm, wm, a, p.tiles, st)
-         : p.mode == kSplit ? launch_linear<TO, GATED, kSplit>(xm, wm, a, p.tiles, st)
-                            : launch_linear<TO, GATED, kOne>(xm, wm, a, p.tiles, st);
+  if constexpr (!lin_exact<TO>)
+    if (p.mode == kPair) return launch_linear<TO, GATED, kPair>(xm, wm, a, p.tiles, st);
+  return p.mode == kSplit ? launch_linear<TO, GATED, kSplit>(xm, wm, a, p.tiles, st)
+                          : launch_linear<TO, GATED, kOne>(xm, wm, a, p.tiles, st);
 }
 
 template <typename TO>
@@ -1059,7 +1161,7 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   a.E = n_experts;
   a.ke = 128 / es;
   a.KB = (K + a.ke - 1) / a.ke;
-  const LinPlan plan = lin_plan(R, N, n_experts, a.KB, gated);
+  const LinPlan plan = lin_plan(R, N, n_experts, a.KB, gated, out_dtype == MOE_DT_F32);
   const int xrows = plan.mode == kPair ? plan.BN / 2 : plan.BN;
   const int ftw = (plan.mode == kPair ? 2 * kLinM : kLinM) / (gated ? 2 : 1);
   a.BN = plan.BN;

@@ -26,10 +26,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxE = 256;
 
-
 // A stable counting sort in one launch: one CTA, or a cluster of eight or sixteen for long id
-// arrays.
-// Each warp owns a contiguous run of slots and counts it into its own row of `hist`; the rows
+// arrays.  Each warp owns a contiguous run of slots and counts it into its own row of `hist`; the rows
 // are scanned over the warps, the CTA totals over the cluster (distributed shared memory), the
 // expert totals over the experts; then each warp walks its run again, 32 slots at a time, and
 // gives a slot the position base + expert's slots so far + equal ids in lower lanes.  The lanes
@@ -472,8 +470,7 @@ int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *of
     return MOE_ERR_INVALID_ARG;
   const int n = T * k;
   // a warp walks its run 32 slots at a time: past two steps a warp, eight CTAs; past four steps
-  // of those, sixteen (65,536 slots: 10.0 us with eight, 8.4 with sixteen;
-  // 262,144: 27.9 and 17.7)
+  // of those, sixteen (65,536 slots: 10.0 us with eight, 8.4 with sixteen; 262,144: 27.9 and 17.7)
   const int ctas = n <= kSortThreads * 2 ? 1 : n <= kSortThreads * 32 ? 8 : 16;
   if (ctas == 16 && cudaFuncSetAttribute(sort_tokens_kernel,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=

@@ -460,6 +460,29 @@ def test_linear_many_rows_or_features(R, N, K, E):
     run_linear(R, N, K, E, F8, TB, "none", True, False, seed=3)
 
 
+@pytest.mark.parametrize("dt", [F8, TB, TH])
+@pytest.mark.parametrize("R,N,K,act", [(1, 256, 14336, "none"), (300, 512, 14336, "none"),
+                                       (700, 256, 6144, "swiglu"), (3000, 512, 4096, "none")])
+def test_linear_fp32_outputs_are_summed_in_fp32(R, N, K, act, dt):
+    """An fp32 output is nearer to the exact product than the tensor cores' truncated sums are.
+
+    Sums of 16 MMAs (4 k-blocks), each truncating by at most 2^-23 of what it holds, on the mean
+    half of that and half of them past the middle: 16 * 2^-25 = 5e-7 of the result, twice that for
+    a product of two; the whole K in tensor memory would lose K / 256 times as much."""
+    rows = 2 * N if act == "swiglu" else N
+    xv, wv = randn(1, R, K), randn(2, rows, K) / math.sqrt(K)
+    xs = ws = None
+    if dt == F8:
+        (x, xs), (w, ws) = rows8(xv), rows8(wv)
+    else:
+        x, w = xv.to(dt), wv.to(dt)
+    out = torch.empty(R, N, device="cuda")
+    moe.moe_linear(x, w, out, x_scale=xs, w_scale=ws, act=act)
+    ref, _ = linear_ref(x, w, xs, ws, None, act, None, None, N)
+    rel = float((out.double() - ref).norm() / ref.norm())
+    assert rel < (2 if act == "swiglu" else 1) * 16 * 2 ** -25 + 4 * U
+
+
 @pytest.mark.parametrize("counts", [[0, 0, 5, 0], [256, 0, 0, 1], [255, 1, 257, 0], [0, 0, 0, 0],
                                     [16, 16, 16, 16], [1, 511, 17, 33]])
 @pytest.mark.parametrize("lead,tail", [(0, 0), (3, 40)])
