@@ -74,14 +74,18 @@ def build(force: bool = False, extra=()) -> str:
     return LIB
 
 
-def _entries_obj(force: bool) -> str:
-    """Compile the token operators' Python entry points (torch's headers, a host compiler)."""
+def _entries_obj(force: bool):
+    """Compile the token operators' Python entry points (torch's headers, a host compiler).
+    None without torch: the C library needs none, and tokens.py cannot be imported then."""
+    try:
+        import torch
+    except ImportError:
+        return None
     src = os.path.join(CSRC, "tokens_py.cpp")
     obj = os.path.join(OUT_DIR, "tokens_py.o")
-    dep = max(os.path.getmtime(p) for p in [src] + _headers())
+    dep = max(os.path.getmtime(p) for p in [src, torch.__file__] + _headers())
     if os.path.exists(obj) and os.path.getmtime(obj) >= dep and not force:
         return obj
-    import torch
     base = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     abi = int(torch.compiled_with_cxx11_abi())
@@ -98,8 +102,10 @@ def _entries_obj(force: bool) -> str:
     return obj
 
 
-def _link_entries(obj: str, force: bool):
+def _link_entries(obj, force: bool):
     """The extension module beside the library it calls; torch's libraries are loaded by torch."""
+    if obj is None:
+        return
     if (os.path.exists(PY_EXT) and not force
             and os.path.getmtime(PY_EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
         return
