@@ -5,16 +5,18 @@
 // ctypes took 5 us, twice the launch, and at decode sizes that is most of the call (7.3 us for a
 // norm of one row, 2.7 this way).  These
 // functions read the tensors through torch's C++ headers, check them, and call the C entry point
-// on the current stream of the operands' device, with the interpreter's lock released.  They
-// return its status; wrong shapes and strides raise ValueError, wrong types TypeError.  They
-// are private: tokens.py documents them.
+// with the operands' device current, on that device's current stream or a given one, with the
+// interpreter's lock released.  They return its status; wrong shapes and strides raise ValueError,
+// wrong types TypeError.  They are private: tokens.py documents them.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "../../include/moe.h"
 
@@ -55,6 +57,73 @@ int size32(int64_t v, const char *name) {
   if (v > 2147483647) raise(PyExc_ValueError, std::string(name) + " is too large");
   return (int)v;
 }
+
+// the interpreter's lock, released for a scope
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// an attribute of a stream object as a Python integer; null where there is none and it may be so
+PyObject *attribute(PyObject *o, const char *name, bool needed) {
+  PyObject *v = PyObject_GetAttrString(o, name);
+  if (v) return v;
+  if (needed || !PyErr_ExceptionMatches(PyExc_AttributeError)) throw Raised{};
+  PyErr_Clear();
+  return nullptr;
+}
+
+// the handle of a torch.cuda.Stream, which must be one of device `dev`
+void *handle(PyObject *stream, int dev) {
+  if (PyObject *d = attribute(stream, "device_index", false)) {
+    const long on = PyLong_AsLong(d);
+    Py_DECREF(d);
+    if (on == -1 && PyErr_Occurred()) throw Raised{};
+    if (on != dev)
+      raise(PyExc_ValueError, "the stream is on device " + std::to_string(on) +
+                                  ", the operands are on device " + std::to_string(dev));
+  }
+  PyObject *h = attribute(stream, "cuda_stream", true);
+  void *s = PyLong_AsVoidPtr(h);
+  Py_DECREF(h);
+  if (PyErr_Occurred()) throw Raised{};
+  return s;
+}
+
+// Runs body(stream) with device `dev`, the operands', current.  A stream's handle does not say
+// where a kernel runs: every device's default stream has the handle 0, and launches, SM counts and
+// kernel attributes go by the calling thread's device.  RT: the CUDA runtime, or its stand-in.
+template <typename RT, typename F>
+long on_device(int dev, PyObject *stream, F body) {
+  if (dev < 0) raise(PyExc_ValueError, "operands must be on a CUDA device");
+  void *st = stream == Py_None ? RT::current(dev) : handle(stream, dev);
+  const typename RT::Guard guard((c10::DeviceIndex)dev);
+  const Unlocked unlocked;
+  return body(st);
+}
+
+struct Cuda {
+  using Guard = c10::cuda::CUDAGuard;
+  static void *current(int dev) {
+    return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+  }
+};
+
+// What a call would do to the runtime, in order, without a GPU (for the tests).
+struct Told {
+  static std::vector<std::string> &steps() {
+    static thread_local std::vector<std::string> s;
+    return s;
+  }
+  struct Guard {
+    explicit Guard(c10::DeviceIndex d) { steps().push_back("set " + std::to_string(d)); }
+    ~Guard() { steps().push_back("restore"); }
+  };
+  static void *current(int dev) {
+    steps().push_back("current stream of " + std::to_string(dev));
+    return nullptr;  // a default stream
+  }
+};
 
 // The operands of one call: all on one CUDA device.
 struct Call {
@@ -105,13 +174,10 @@ struct Call {
                      std::initializer_list<int64_t> shape) const {
     return o == Py_None ? nullptr : flat(o, name, type, shape);
   }
-  // the given stream's handle, or the current stream of the operands' device
-  void *stream(PyObject *o) const {
-    if (dev < 0) raise(PyExc_ValueError, "operands must be on a CUDA device");
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    void *s = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) throw Raised{};
-    return s;
+  // body(stream) on the operands' device
+  template <typename F>
+  long launch(PyObject *stream, F body) const {
+    return on_device<Cuda>(dev, stream, body);
   }
 };
 
@@ -143,12 +209,6 @@ PyObject *run(Py_ssize_t n, Py_ssize_t want, F body) {
   }
   return nullptr;
 }
-// the interpreter's lock, released for a scope
-struct Unlocked {
-  PyThreadState *state = PyEval_SaveThread();
-  ~Unlocked() { PyEval_RestoreThread(state); }
-};
-
 // x, q, scale, add, weight, resid, eps, group, normalize, stream
 PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 10, [&]() {
@@ -169,10 +229,10 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *pr = c.rows_or_null(a[5], "resid", dt, T, H, ldr);
     const int rt = row_type(dt);
     const int t32 = size32(T, "x"), h32 = size32(H, "x");
-    void *st = c.stream(a[9]);
-    const Unlocked unlocked;
-    return moe_rmsnorm_e4m3(t32, h32, px, ldx, (moe_dtype)rt, pa, lda, pw, eps, normalize,
-                            group, pr, ldr, pq, ldq, ps, st);
+    return c.launch(a[9], [&](void *st) {
+      return moe_rmsnorm_e4m3(t32, h32, px, ldx, (moe_dtype)rt, pa, lda, pw, eps, normalize,
+                              group, pr, ldr, pq, ldq, ps, st);
+    });
   });
 }
 
@@ -187,9 +247,9 @@ PyObject *sort(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *pp = (int32_t *)c.flat(a[3], "perm", at::kInt, {T * k});
     int32_t *ps = (int32_t *)c.flat(a[4], "slot_pos", at::kInt, {T, k});
     const int t32 = size32(T, "ids"), k32 = size32(k, "ids"), e32 = size32(E, "n_experts");
-    void *st = c.stream(a[5]);
-    const Unlocked unlocked;
-    return moe_sort_tokens(t32, k32, e32, pi, po, pp, ps, st);
+    return c.launch(a[5], [&](void *st) {
+      return moe_sort_tokens(t32, k32, e32, pi, po, pp, ps, st);
+    });
   });
 }
 
@@ -218,10 +278,10 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int rt = row_type(dt), t32 = size32(T, "x"), k32 = size32(k, "slot_pos");
     const int h32 = size32(H, "x"), s32 = size32(S, "scale"), e32 = size32(E1 - 1, "offsets");
-    void *st = c.stream(a[6]);
-    const Unlocked unlocked;
-    return moe_dispatch_rows(t32, k32, e32, h32, (moe_dtype)rt, px, ldx, pp, po, pxs, s32, psc,
-                             ldsc, pss, st);
+    return c.launch(a[6], [&](void *st) {
+      return moe_dispatch_rows(t32, k32, e32, h32, (moe_dtype)rt, px, ldx, pp, po, pxs, s32, psc,
+                               ldsc, pss, st);
+    });
   });
 }
 
@@ -241,10 +301,10 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const void *pa = c.rows_or_null(a[4], "add", ot, T, H, lda);
     const int ry = row_type(yt), ro = row_type(ot), t32 = size32(T, "slot_pos");
     const int k32 = size32(k, "slot_pos"), h32 = size32(H, "out");
-    void *st = c.stream(a[5]);
-    const Unlocked unlocked;
-    return moe_combine_rows(t32, k32, h32, py, (moe_dtype)ry, pp, pw, pa, lda, po, ldo,
-                            (moe_dtype)ro, st);
+    return c.launch(a[5], [&](void *st) {
+      return moe_combine_rows(t32, k32, h32, py, (moe_dtype)ry, pp, pw, pa, lda, po, ldo,
+                              (moe_dtype)ro, st);
+    });
   });
 }
 
@@ -266,10 +326,10 @@ PyObject *combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     float *pdw = (float *)c.flat(a[6], "dw", at::kFloat, {T, k});
     const int rt = row_type(dt), t32 = size32(T, "slot_pos"), k32 = size32(k, "slot_pos");
     const int h32 = size32(H, "dout"), e32 = size32(E1 - 1, "offsets");
-    void *st = c.stream(a[7]);
-    const Unlocked unlocked;
-    return moe_combine_rows_grad(t32, k32, e32, h32, (moe_dtype)rt, pd, ldd, py, pp, po, pw, pdy,
-                                 pdw, st);
+    return c.launch(a[7], [&](void *st) {
+      return moe_combine_rows_grad(t32, k32, e32, h32, (moe_dtype)rt, pd, ldd, py, pp, po, pw,
+                                   pdy, pdw, st);
+    });
   });
 }
 
@@ -287,10 +347,10 @@ PyObject *dispatch_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *px = c.rows(a[2], "dx", xt, T, H, ldx);
     const int rd = row_type(dt), rx = row_type(xt), t32 = size32(T, "slot_pos");
     const int k32 = size32(k, "slot_pos"), h32 = size32(H, "dx");
-    void *st = c.stream(a[3]);
-    const Unlocked unlocked;
-    return moe_dispatch_rows_grad(t32, k32, h32, (moe_dtype)rd, pd, pp, px, ldx, (moe_dtype)rx,
-                                  st);
+    return c.launch(a[3], [&](void *st) {
+      return moe_dispatch_rows_grad(t32, k32, h32, (moe_dtype)rd, pd, pp, px, ldx, (moe_dtype)rx,
+                                    st);
+    });
   });
 }
 
@@ -329,17 +389,37 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *pst = (int32_t *)c.flat_or_null(a[9], "status", at::kInt, {1});
     const int rt = row_type(dt), ro = row_type(ot), r32 = size32(R, "x"), n32 = size32(N, "out");
     const int k32 = size32(K, "x"), e32 = size32(E, "offsets");
-    void *st = c.stream(a[10]);
-    const Unlocked unlocked;
-    return moe_linear(r32, n32, k32, e32, px, ldx, (moe_dtype)rt, pxs, pw, pws, pb, (moe_act)act,
-                      pr, ldr, po, pout, ldo, (moe_dtype)ro, pst, st);
+    return c.launch(a[10], [&](void *st) {
+      return moe_linear(r32, n32, k32, e32, px, ldx, (moe_dtype)rt, pxs, pw, pws, pb,
+                        (moe_act)act, pr, ldr, po, pout, ldo, (moe_dtype)ro, pst, st);
+    });
   });
+}
+
+// dev, stream -> what a call with operands on device `dev` does
+PyObject *trace(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  Told::steps().clear();
+  PyObject *r = run(n, 2, [&]() {
+    return on_device<Told>(number32(a[0], "dev"), a[1], [](void *st) {
+      Told::steps().push_back("call on " + std::to_string((uintptr_t)st));
+      return 0;
+    });
+  });
+  if (!r) return nullptr;
+  Py_DECREF(r);
+  PyObject *out = PyList_New(0);
+  for (const std::string &t : Told::steps()) {
+    PyObject *v = out ? PyUnicode_FromString(t.c_str()) : nullptr;
+    if (!v || PyList_Append(out, v) < 0) Py_CLEAR(out);
+    Py_XDECREF(v);
+  }
+  return out;
 }
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(rmsnorm),      METHOD(sort),          METHOD(dispatch),
                          METHOD(combine),      METHOD(combine_grad),  METHOD(dispatch_grad),
-                         METHOD(linear),       {nullptr, nullptr, 0, nullptr}};
+                         METHOD(linear),       METHOD(trace),         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens_native", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

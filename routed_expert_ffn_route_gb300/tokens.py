@@ -2,7 +2,8 @@
 
 RMS norm to e4m3 rows, tokens sorted by expert and back with gradients, and the matrix
 product with its epilogue.  As in the rest of the package every step runs in the library's
-kernels, on the current stream, into tensors that the caller owns; nothing is allocated and
+kernels, on the operands' device (which need not be the current one) and its current stream or a
+given torch.cuda.Stream of that device, into tensors that the caller owns; nothing is allocated and
 every call may be captured into a graph.  Shapes, types, strides and devices are checked (the
 C entry points see only addresses): a wrong one raises ValueError or TypeError, an error of the
 C entry point MoEError.
@@ -40,45 +41,41 @@ def _check(status, where):
         raise MoEError(status, where)
 
 
-def _handle(stream):
-    return None if stream is None else stream.cuda_stream
-
-
 def moe_rmsnorm_e4m3(x, q, scale, add=None, weight=None, resid=None, eps=1e-6, group=0,
                      normalize=True, stream=None):
     """r = x + add -> resid; q (float8_e4m3fn [T, H]) and scale (fp32 [T, ceil(H / group)],
     group 0: one a row) of r * weight / sqrt(mean(r^2) + eps).  normalize=False quantises
     r * weight itself.  x, add, resid [T, H] and weight [H] of one type, rows may lie apart."""
     _check(_native.rmsnorm(x, q, scale, add, weight, resid, eps, group, normalize,
-                           _handle(stream)), "moe_rmsnorm_e4m3")
+                           stream), "moe_rmsnorm_e4m3")
 
 
 def moe_sort_tokens(ids, n_experts, offsets, perm, slot_pos, stream=None):
     """ids int32 [T, k] -> offsets [E + 1], perm [T * k], slot_pos [T, k], all int32."""
-    _check(_native.sort(ids, n_experts, offsets, perm, slot_pos, _handle(stream)),
+    _check(_native.sort(ids, n_experts, offsets, perm, slot_pos, stream),
            "moe_sort_tokens")
 
 
 def moe_dispatch_rows(x, slot_pos, offsets, xs, scale=None, scale_s=None, stream=None):
     """xs[slot_pos[t, j]] = x[t] ([T * k, H], the rest zero); scale [T, S] -> scale_s alike."""
-    _check(_native.dispatch(x, slot_pos, offsets, xs, scale, scale_s, _handle(stream)),
+    _check(_native.dispatch(x, slot_pos, offsets, xs, scale, scale_s, stream),
            "moe_dispatch_rows")
 
 
 def moe_combine_rows(y, slot_pos, out, w=None, add=None, stream=None):
     """out[t] = add[t] + sum_j w[t, j] * y[slot_pos[t, j]] (slots of -1 left out)."""
-    _check(_native.combine(y, slot_pos, out, w, add, _handle(stream)), "moe_combine_rows")
+    _check(_native.combine(y, slot_pos, out, w, add, stream), "moe_combine_rows")
 
 
 def moe_combine_rows_grad(dout, y, slot_pos, offsets, w, dy, dw, stream=None):
     """dy[slot_pos[t, j]] = w[t, j] * dout[t] (the rest zero), dw[t, j] = <dout[t], y[slot]>."""
-    _check(_native.combine_grad(dout, y, slot_pos, offsets, w, dy, dw, _handle(stream)),
+    _check(_native.combine_grad(dout, y, slot_pos, offsets, w, dy, dw, stream),
            "moe_combine_rows_grad")
 
 
 def moe_dispatch_rows_grad(dxs, slot_pos, dx, stream=None):
     """dx[t] = sum_j dxs[slot_pos[t, j]] (slots of -1 left out)."""
-    _check(_native.dispatch_grad(dxs, slot_pos, dx, _handle(stream)), "moe_dispatch_rows_grad")
+    _check(_native.dispatch_grad(dxs, slot_pos, dx, stream), "moe_dispatch_rows_grad")
 
 
 def moe_linear(x, w, out, x_scale=None, w_scale=None, bias=None, act="none", residual=None,
@@ -92,4 +89,4 @@ def moe_linear(x, w, out, x_scale=None, w_scale=None, bias=None, act="none", res
     if code is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     _check(_native.linear(x, w, out, x_scale, w_scale, bias, code, residual, offsets, status,
-                          _handle(stream)), "moe_linear")
+                          stream), "moe_linear")
