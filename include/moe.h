@@ -370,6 +370,14 @@ int moe_linear(int R, int N, int K, int n_experts, const void *x, long ldx, moe_
                moe_act act, const void *residual, long ldres, const int32_t *offsets, void *out,
                long ldout, moe_dtype out_dtype, int32_t *status, void *stream);
 
+/* Test hook: moe_linear whose epilogue waits for what nothing completes, with no time to wait, so
+ * that its waits run out: *status becomes MOE_ERR_TIMEOUT, the rows of experts are not written. */
+int moe_debug_linear_timeout(int R, int N, int K, int n_experts, const void *x, long ldx,
+                             moe_dtype dtype, const float *x_scale, const void *w,
+                             const float *w_scale, const float *bias, moe_act act,
+                             const void *residual, long ldres, const int32_t *offsets, void *out,
+                             long ldout, moe_dtype out_dtype, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,7 +43,7 @@ EXPORTED = [
     "moe_layer_forward_static", "moe_residual_rmsnorm", "moe_quantize_rows",
     "moe_layer_forward_experts", "moe_layer_forward_next", "moe_rmsnorm_e4m3",
     "moe_sort_tokens", "moe_dispatch_rows", "moe_dispatch_rows_grad", "moe_combine_rows",
-    "moe_combine_rows_grad", "moe_linear",
+    "moe_combine_rows_grad", "moe_linear", "moe_debug_linear_timeout",
 ]
 _TOKEN_OPERATORS = ("moe_rmsnorm_e4m3", "moe_sort_tokens", "moe_dispatch_rows",
                     "moe_dispatch_rows_grad", "moe_combine_rows", "moe_combine_rows_grad",
@@ -130,6 +130,7 @@ def _bind(L):
         "moe_dispatch_rows_grad": (I, [I, I, I, I, P, P, P, N, I, P]),
         "moe_linear": (I, [I, I, I, I, P, N, I, P, P, P, P, I, P, N, P, P, N, I, P, P]),
     }
+    sig["moe_debug_linear_timeout"] = sig["moe_linear"]
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res

@@ -46,6 +46,7 @@ constexpr int kLinRing = 192 * 1024;  // shared memory of the ring and the excha
 constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk (32 features)
 constexpr int kLinStage = kLinEpi * 16 * kLinPitch * 4;  // bytes of the staged chunks
 constexpr long kLinWaitNs = 2000000000L;
+constexpr long kLinLateNs = 50000000L;  // a pair's copies, after a wait gave up
 
 // fp32 outputs: the tensor cores truncate each sum to fp32 (K = 6144 bf16 loses 6e-6 of the result
 // that way, 1.4e-5 of a SwiGLU's), so they sum kLinExact k-blocks at a time and the epilogue warps
@@ -89,12 +90,15 @@ struct LinArgs {
   int act;
   int kind8, bf16;   // operand type: e4m3, or bf16 / fp16
   int vec;           // out's and residual's rows start on 16-byte boundaries
+  int never;         // the epilogue's waits run out (moe_debug_linear_timeout)
 };
 
 struct alignas(16) LinBars {
-  uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain, never;
   uint32_t tmem;
   int abort_flag;
+  uint32_t armed, phases;  // for the drain: stages with a copy started, and their last phase
+  int issued;              // some MMA was issued
   alignas(16) float xs[kLinEpi][kLinMaxN / 2];     // token scales of the epilogue warps' columns
   int pre[kLinMaxE + 1];   // row tiles before each expert
   int off[kLinMaxE + 1];   // first row of each expert
@@ -528,20 +532,65 @@ struct LinOut16 {
   }
 };
 
+// ---------------------------------------------------------------- waits that give up
+// A wait gave up: the CTA's (PAIR: both CTAs') other waits end too, and the caller is told.  A
+// limit runs out by the clock, so this may be the only role that sees it (the others may have
+// finished, or go on when the GPU comes back to this context): whichever wait it is has to say so.
+template <bool PAIR>
+__device__ __forceinline__ void lin_give_up(const LinArgs &a, LinBars *b, uint32_t rank) {
+  *(volatile int *)&b->abort_flag = 1;
+  if (PAIR)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(&b->abort_flag, rank ^ 1)), "r"(1)
+                 : "memory");
+  if (a.status) *a.status = MOE_ERR_TIMEOUT;
+}
+
+// the epilogue's wait for accumulator `buf`: in the test hook, for what nothing completes
+__device__ __forceinline__ bool lin_wait_acc(const LinArgs &a, LinBars *b, int buf, uint32_t parity,
+                                             volatile int *abort, uint32_t sleep_ns) {
+  uint64_t *bar = a.never ? &b->never : &b->acc_full[buf];
+  return __all_sync(0xffffffffu, tc::mbar_wait_backoff(bar, parity, abort,
+                                                       a.never ? 0 : kLinWaitNs, sleep_ns));
+}
+
+// After a wait gave up and every role has left: copies and MMAs that were started end before the
+// CTA frees its tensor memory and exits.  (Without a failure the epilogue's waits have seen to it.)
+template <bool PAIR>
+__device__ __noinline__ void lin_drain(LinBars *b, int stages, uint32_t rank, int warp, int lane) {
+  if (warp == 0 && lane == 0) {
+    // PAIR: the leader's barriers count both CTAs' copies; one that the second CTA had not started
+    // is not worth a long wait
+    for (int q = 0; q < stages; q++)
+      if ((b->armed >> q) & 1)
+        wait_nofail(&b->full[q], (b->phases >> q) & 1, PAIR ? kLinLateNs : kLinWaitNs);
+    // the second CTA of a pair has no barrier of its own to wait on: its copies are loads of
+    // some microseconds
+    if (PAIR && rank) for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  } else if (warp == 1) {
+    // the lane that issued the MMAs: elect gives the same one every time
+    const bool leader = tc::elect_one();
+    if (leader && b->issued) {
+      lin_commit<PAIR>(&b->drain);
+      wait_nofail(&b->drain, 0, kLinWaitNs);
+    } else if (leader && PAIR && rank) {  // the leader's MMAs read this CTA's stages too
+      wait_nofail(&b->drain, 0, kLinLateNs);
+    }
+    __syncwarp();
+  }
+}
+
 // fp32 outputs: this warp's chunks of 16 columns (every second one of a tile's, NI of them at
 // most), summed over the accumulators of a tile's k-blocks; false when a wait gave up
 template <int NI, int ACC>
-__device__ __forceinline__ bool lin_sum(LinBars *b, uint32_t taddr, int n, int half, int lane,
-                                        int kblocks, int &buf, uint32_t &bph, float (&sum)[NI][16],
-                                        volatile int *abort) {
+__device__ __forceinline__ bool lin_sum(const LinArgs &a, LinBars *b, uint32_t taddr, int n,
+                                        int half, int lane, int kblocks, int &buf, uint32_t &bph,
+                                        float (&sum)[NI][16], volatile int *abort) {
 #pragma unroll
   for (int i = 0; i < NI; i++)
 #pragma unroll
     for (int j = 0; j < 16; j++) sum[i][j] = 0.f;
   for (int k0 = 0; k0 < kblocks; k0 += kLinExact) {
-    if (!__all_sync(0xffffffffu,
-                    tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 32)))
-      return false;
+    if (!lin_wait_acc(a, b, buf, bph, abort, 32)) return false;
     tc::fence_after_sync();
 #pragma unroll
     for (int i = 0; i < NI; i++) {
@@ -604,15 +653,18 @@ __device__ __forceinline__ void lin_epilogue(const LinArgs &a, LinBars *b, uint3
     }
     if constexpr (EXACT) {
       float sum[kLinExactN / 32][16];
-      if (!lin_sum<kLinExactN / 32, kLinAcc<float>>(b, tbase + ((uint32_t)(32 * quad) << 16), n,
-                                                    half, lane, a.KB, buf, bph, sum, abort))
+      if (!lin_sum<kLinExactN / 32, kLinAcc<float>>(a, b, tbase + ((uint32_t)(32 * quad) << 16), n,
+                                                    half, lane, a.KB, buf, bph, sum, abort)) {
+        if (lane == 0) lin_give_up<PAIR>(a, b, rank);
         break;
+      }
       now.tile_sums(sum, n, half, lane, xs);
       continue;
     }
-    if (!__all_sync(0xffffffffu,
-                    tc::mbar_wait_backoff(&b->acc_full[buf], bph, abort, kLinWaitNs, 64)))
+    if (!lin_wait_acc(a, b, buf, bph, abort, 64)) {
+      if (lane == 0) lin_give_up<PAIR>(a, b, rank);
       break;
+    }
     tc::fence_after_sync();
     now.tile(tbase + buf * kLinMaxN + ((uint32_t)(32 * quad) << 16), n, half, lane, xs);
     // the accumulator is read: the next tile may use it
@@ -660,7 +712,10 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
       tc::mbar_init(&b->acc_empty[i], PAIR ? 2 * kLinEpi : kLinEpi);
     }
     tc::mbar_init(&b->drain, 1);
+    tc::mbar_init(&b->never, 1);
     b->abort_flag = 0;
+    b->armed = b->phases = 0;
+    b->issued = 0;
     tc::fence_barrier_init();
   }
   __syncwarp();
@@ -707,14 +762,6 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
   tc::fence_after_sync();
   const uint32_t tbase = b->tmem;
   volatile int *abort = &b->abort_flag;
-  auto give_up = [&]() {
-    *abort = 1;
-    if (PAIR)
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(&b->abort_flag, rank ^ 1)),
-                   "r"(1)
-                   : "memory");
-    if (a.status) *a.status = MOE_ERR_TIMEOUT;
-  };
   // the tiles of this CTA (pair, cluster), and its part of K
   const int total = b->pre[max(1, a.E)] * a.FT;
   const int cta = PAIR ? blockIdx.x / 2 : SPLIT ? blockIdx.x / a.split : blockIdx.x;
@@ -752,14 +799,9 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
           if (++s == a.stages) s = 0, ph ^= 1;
         }
       }
-      if (!ok) {  // every copy started lands before the CTA exits
-        give_up();
-        for (int q = 0; q < a.stages; q++)
-          if ((armed >> q) & 1) wait_nofail(&b->full[q], (last_ph >> q) & 1, kLinWaitNs);
-        // the second CTA of a pair has no barrier of its own to wait on: its copies are loads
-        // of some microseconds
-        if (PAIR && rank) for (int i = 0; i < 1000; i++) __nanosleep(1000);
-      }
+      b->armed = armed;
+      b->phases = last_ph;
+      if (!ok) lin_give_up<PAIR>(a, b, rank);
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (one elected lane)
@@ -808,12 +850,9 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
         buf ^= 1;
       }
     }
-    if (leader && !ok) {
-      give_up();
-      if (issued) {  // every MMA issued completes before the tensor memory is freed
-        lin_commit<PAIR>(&b->drain);
-        wait_nofail(&b->drain, 0, kLinWaitNs);
-      }
+    if (leader) {
+      b->issued = issued;
+      if (!ok) lin_give_up<PAIR>(a, b, rank);
     }
   } else if (!SPLIT) {
     if (sizeof(TO) == 2 && !a.residual)
@@ -846,13 +885,13 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
       if constexpr (lin_exact<TO>) {
         int buf = 0;
         uint32_t bph = 0;
-        ok = lin_sum<kLinExactSplitN / 32, kLinAcc<TO>>(b, taddr, t.n, half, lane, kb1 - kb0, buf,
-                                                       bph, sum, abort);
+        ok = lin_sum<kLinExactSplitN / 32, kLinAcc<TO>>(a, b, taddr, t.n, half, lane, kb1 - kb0,
+                                                       buf, bph, sum, abort);
       } else {
-        ok = __all_sync(0xffffffffu,
-                        tc::mbar_wait_backoff(&b->acc_full[0], 0, abort, kLinWaitNs, 32));
+        ok = lin_wait_acc(a, b, 0, 0, abort, 32);
         tc::fence_after_sync();
       }
+      if (!ok && lane == 0) lin_give_up<PAIR>(a, b, rank);
     }
     __syncwarp();
     cluster_wait();  // every CTA of the cluster has started: its memory may be written
@@ -925,6 +964,12 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
   tc::fence_before_sync();
   if (PAIR) cluster_sync(); else __syncthreads();  // nobody still uses a peer's barriers
   tc::fence_after_sync();
+  if (*abort) {  // the same for all threads: every role has left
+    lin_drain<PAIR>(b, a.stages, rank, warp, lane);
+    tc::fence_before_sync();
+    if (PAIR) cluster_sync(); else __syncthreads();
+    tc::fence_after_sync();
+  }
   if (warp == 0) lin_tmem_free<MODE>(tbase);
 }
 
@@ -1113,15 +1158,13 @@ static int launch_linear_t(const CUtensorMap &xm, const CUtensorMap &wm, const L
                                  : launch_linear_m<TO, false>(xm, wm, a, p, st);
 }
 
-}  // namespace moe
-
-using namespace moe;
-
-extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, long ldx,
-                          moe_dtype dtype, const float *x_scale, const void *w,
-                          const float *w_scale, const float *bias, moe_act act,
-                          const void *residual, long ldres, const int32_t *offsets, void *out,
-                          long ldout, moe_dtype out_dtype, int32_t *status, void *stream) {
+// moe_linear; `never`: whose epilogue's waits run out
+static int linear_call(int R, int N, int K, int n_experts, const void *x, long ldx,
+                       moe_dtype dtype, const float *x_scale, const void *w,
+                       const float *w_scale, const float *bias, moe_act act,
+                       const void *residual, long ldres, const int32_t *offsets, void *out,
+                       long ldout, moe_dtype out_dtype, int32_t *status, int never,
+                       void *stream) {
   if (R < 0 || N <= 0 || K <= 0 || n_experts < 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_DT_E4M3 && dtype != MOE_DT_BF16 && dtype != MOE_DT_F16)
     return MOE_ERR_INVALID_ARG;
@@ -1154,6 +1197,7 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
   a.out = out;
   a.offsets = n_experts ? offsets : nullptr;
   a.status = status;
+  a.never = never;
   a.ldres = ldres;
   a.ldout = ldout;
   a.R = R;
@@ -1221,3 +1265,28 @@ extern "C" int moe_linear(int R, int N, int K, int n_experts, const void *x, lon
          : out_dtype == MOE_DT_BF16 ? launch_linear_t<__nv_bfloat16>(xm, wm, a, plan, st)
                                     : launch_linear_t<__half>(xm, wm, a, plan, st);
 }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_linear(int R, int N, int K, int n_experts, const void *x, long ldx, moe_dtype dtype,
+               const float *x_scale, const void *w, const float *w_scale, const float *bias,
+               moe_act act, const void *residual, long ldres, const int32_t *offsets, void *out,
+               long ldout, moe_dtype out_dtype, int32_t *status, void *stream) {
+  return linear_call(R, N, K, n_experts, x, ldx, dtype, x_scale, w, w_scale, bias, act, residual,
+                     ldres, offsets, out, ldout, out_dtype, status, 0, stream);
+}
+
+int moe_debug_linear_timeout(int R, int N, int K, int n_experts, const void *x, long ldx,
+                             moe_dtype dtype, const float *x_scale, const void *w,
+                             const float *w_scale, const float *bias, moe_act act,
+                             const void *residual, long ldres, const int32_t *offsets, void *out,
+                             long ldout, moe_dtype out_dtype, int32_t *status, void *stream) {
+  return linear_call(R, N, K, n_experts, x, ldx, dtype, x_scale, w, w_scale, bias, act, residual,
+                     ldres, offsets, out, ldout, out_dtype, status, 1, stream);
+}
+
+}  // extern "C"
