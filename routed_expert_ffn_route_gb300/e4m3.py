@@ -10,12 +10,14 @@ experts that are kept as 8-bit floating-point rows, routed by the same router:
     out = r + sum_j w[t, j] * (h Wd_e^T)[row of (t, j)]
 
 Every step runs in the library's kernels on buffers that this object owns, so that a step can
-be captured in a CUDA graph.
+be captured in a CUDA graph.  What the device finds out on the way (a bounded wait that gave up:
+the output is then undefined) stays in a status word until read_status() takes it.
 """
 from __future__ import annotations
 
 import torch
 
+from . import MOE_OK
 from .tokens import (moe_combine_rows, moe_dispatch_rows, moe_linear, moe_rmsnorm_e4m3,
                      moe_sort_tokens)
 
@@ -56,6 +58,7 @@ class E4m3Experts:
         self.h = torch.empty((n, self.I), dtype=dtype, **on)
         self.hq, self.hs = torch.empty((n, self.I), dtype=E4M3, **on), torch.empty((n, 1), **on)
         self.y = torch.empty((n, H), dtype=dtype, **on)
+        self.status = torch.zeros(1, **i32)
 
     def forward(self, resid, add, ids, w):
         """resid [T, H] and add (the attention's output, or None) of the layer's dtype, ids int32
@@ -72,8 +75,17 @@ class E4m3Experts:
         moe_sort_tokens(ids, self.E, self.offsets, self.perm[:n], pos)
         moe_dispatch_rows(q, pos, self.offsets, xs, scale=qs, scale_s=xss)
         moe_linear(xs, self.w1, h, x_scale=xss, w_scale=self.s1, act="swiglu",
-                   offsets=self.offsets)
+                   offsets=self.offsets, status=self.status)
         moe_rmsnorm_e4m3(h, hq, hs, normalize=False)
-        moe_linear(hq, self.w2, y, x_scale=hs, w_scale=self.s2, offsets=self.offsets)
+        moe_linear(hq, self.w2, y, x_scale=hs, w_scale=self.s2, offsets=self.offsets,
+                   status=self.status)
         moe_combine_rows(y, pos, out, w=w, add=r)
         return out
+
+    def read_status(self):
+        """The status of the forward calls since the last reading (MOE_OK, or MOE_ERR_TIMEOUT when
+        one's output is undefined), cleared by it.  Waits for the current stream."""
+        status = int(self.status)
+        if status != MOE_OK:
+            self.status.zero_()
+        return status
