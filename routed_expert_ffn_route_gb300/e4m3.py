@@ -48,15 +48,15 @@ class E4m3Experts:
         self.E, self.I, self.H, self.k, self.t_max = E, I2 // 2, H, top_k, t_max
         self.norm_weight, self.eps, self.dtype = norm_weight, eps, dtype
         n, on = t_max * top_k, {"device": gate_up.device}
-        i32 = {"dtype": torch.int32, **on}
+        i32, f32 = {"dtype": torch.int32, **on}, {"dtype": torch.float32, **on}
         self.resid = torch.empty((t_max, H), dtype=dtype, **on)
         self.out = torch.empty((t_max, H), dtype=dtype, **on)
-        self.q, self.qs = torch.empty((t_max, H), dtype=E4M3, **on), torch.empty((t_max, 1), **on)
+        self.q, self.qs = torch.empty((t_max, H), dtype=E4M3, **on), torch.empty((t_max, 1), **f32)
         self.offsets = torch.empty(E + 1, **i32)
         self.perm, self.slot_pos = torch.empty(n, **i32), torch.empty((t_max, top_k), **i32)
-        self.xs, self.xss = torch.empty((n, H), dtype=E4M3, **on), torch.empty((n, 1), **on)
+        self.xs, self.xss = torch.empty((n, H), dtype=E4M3, **on), torch.empty((n, 1), **f32)
         self.h = torch.empty((n, self.I), dtype=dtype, **on)
-        self.hq, self.hs = torch.empty((n, self.I), dtype=E4M3, **on), torch.empty((n, 1), **on)
+        self.hq, self.hs = torch.empty((n, self.I), dtype=E4M3, **on), torch.empty((n, 1), **f32)
         self.y = torch.empty((n, H), dtype=dtype, **on)
         self.status = torch.zeros(1, **i32)
 

@@ -65,3 +65,15 @@ def test_status_of_a_step_and_of_a_graph():
     layer.status.fill_(moe.MOE_ERR_TIMEOUT)
     g.replay()
     assert layer.read_status() == moe.MOE_ERR_TIMEOUT and layer.read_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("default", [torch.float32, torch.bfloat16, torch.float64])
+def test_buffers_do_not_follow_torchs_default_type(default, calls):
+    """Scales are fp32 whatever the program's default type is (models often set bf16)."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        layer = layer_on("cpu")
+    finally:
+        torch.set_default_dtype(before)
+    assert {layer.qs.dtype, layer.xss.dtype, layer.hs.dtype} == {torch.float32}
