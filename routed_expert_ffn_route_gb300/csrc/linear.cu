@@ -24,13 +24,13 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 
 #include "dev.cuh"
 #include "elem.cuh"
 #include "expert_args.cuh"
+#include "host.cuh"
 #include "moe_internal.cuh"
 #include "tc.cuh"
 
@@ -1016,34 +1016,36 @@ static LinSplit lin_split(int BN, int split, int KB) {
   return r;
 }
 
-// Clusters of `split` CTAs that run at the same time with one CTA on an SM
+// Clusters of `split` CTAs that run at the same time on the current device with one CTA on an SM
+// (0 where none do, or the query fails: the plan does without them)
 static int lin_clusters(int split) {
-  static std::atomic<int> known[3];
-  std::atomic<int> &k = known[split == 2 ? 0 : split == 4 ? 1 : 2];
-  int n = k.load(std::memory_order_relaxed);
-  if (n) return n;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)split * dev_info().sms);
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>(kLinRing);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) !=
-      cudaSuccess) {
-    cudaGetLastError();  // not an error of the call: the plan does without clusters
-    n = 0;
-  }
-  n = std::max(1, n);
-  k.store(n, std::memory_order_relaxed);
-  return n;
+  static DeviceAnswers known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return known.get(dev, split, [&]() {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split * dev_info().sms);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = lin_smem<float, false, kSplit>(kLinRing);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<float, false, kSplit>, &cfg) !=
+        cudaSuccess) {
+      cudaGetLastError();  // not an error of the call
+      n = 0;
+    }
+    return n;
+  });
 }
 
 struct LinPlan {
   int mode, BN, split;
   long tiles;
+  bool sure;  // made with every answer
 };
 
 // How to cut the product: an estimate in SM cycles of each candidate, from what was measured.
@@ -1060,6 +1062,8 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated, bool exact
   const double active = E > 1 ? E * (1.0 - std::pow(1.0 - 1.0 / E, R)) : 1.0;
   const double m = R / active;
   const int rows = gated ? 2 * N : N;
+  const int clusters[3] = {lin_clusters(2), lin_clusters(4), lin_clusters(8)};
+  const bool sure = clusters[0] > 0 && clusters[1] > 0 && clusters[2] > 0;
   LinPlan best{};
   double cost = 1e30;
   for (int mode = 0; mode < 3; mode++)
@@ -1080,7 +1084,8 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated, bool exact
         double c;
         if (mode == kSplit) {  // one tile a cluster
           const LinSplit sp = lin_split(BN, split, KB);
-          if (sp.stages < 2 || tiles > lin_clusters(split) * (sp.two ? 2 : 1)) continue;
+          const int fit = clusters[split == 2 ? 0 : split == 4 ? 1 : 2];
+          if (sp.stages < 2 || tiles > fit * (sp.two ? 2 : 1)) continue;
           const double shared = tiles * split > sms ? 1.25 : 1.0;  // some SMs have two CTAs
           c = (KB + split - 1) / split * kb * shared + 2000 + 12.0 * BN * (split - 1);
         } else {
@@ -1090,7 +1095,7 @@ static LinPlan lin_make_plan(int R, int N, int E, int KB, bool gated, bool exact
         }
         if (c < cost * 0.999) {
           cost = c;
-          best = LinPlan{mode, BN, split, 0};
+          best = LinPlan{mode, BN, split, 0, sure};
         }
       }
   const int FT = (rows + (best.mode == kPair ? 255 : 127)) / (best.mode == kPair ? 256 : 128);
@@ -1115,8 +1120,9 @@ static LinPlan lin_plan(int R, int N, int E, int KB, bool gated, bool exact) {
   Entry &e = seen[(h >> 16) & 63];
   if (e.R == R && e.N == N && e.E == E && e.KB == KB && e.form == form && e.dev == dev)
     return e.plan;
-  e = Entry{R, N, E, KB, form, dev, lin_make_plan(R, N, E, KB, gated, exact)};
-  return e.plan;
+  const LinPlan plan = lin_make_plan(R, N, E, KB, gated, exact);
+  if (plan.sure) e = Entry{R, N, E, KB, form, dev, plan};
+  return plan;
 }
 
 template <typename TO, bool GATED, int MODE>
