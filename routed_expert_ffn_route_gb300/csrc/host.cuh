@@ -27,4 +27,15 @@ class DeviceAnswers {
   std::unordered_map<long, int> known_;
 };
 
+// CTAs of a sort of n slots: a warp walks its run 32 slots at a time, so past two steps a warp of
+// one CTA (1024 threads) a cluster of eight, past four steps of those sixteen.  launch(ctas) returns
+// 0 when it started; a cluster of sixteen is more than every device and context must have room for
+// (one that owns part of the SMs may not), so where it is refused eight do the same work.
+template <typename F>
+int sort_launch(long n, F launch) {
+  const int ctas = n <= 1024 * 2 ? 1 : n <= 1024 * 32 ? 8 : 16;
+  const int e = launch(ctas);
+  return e != 0 && ctas == 16 ? launch(8) : e;
+}
+
 }  // namespace moe

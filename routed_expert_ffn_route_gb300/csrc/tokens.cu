@@ -15,6 +15,7 @@
 
 #include "dev.cuh"
 #include "elem.cuh"
+#include "host.cuh"
 #include "moe_internal.cuh"
 
 namespace cg = cooperative_groups;
@@ -469,32 +470,33 @@ int moe_sort_tokens(int T, int k, int n_experts, const int32_t *ids, int32_t *of
   if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)perm | (uintptr_t)slot_pos) % 4)
     return MOE_ERR_INVALID_ARG;
   const int n = T * k;
-  // a warp walks its run 32 slots at a time: past two steps a warp, eight CTAs; past four steps
-  // of those, sixteen (65,536 slots: 10.0 us with eight, 8.4 with sixteen; 262,144: 27.9 and 17.7)
-  const int ctas = n <= kSortThreads * 2 ? 1 : n <= kSortThreads * 32 ? 8 : 16;
-  if (ctas == 16 && cudaFuncSetAttribute(sort_tokens_kernel,
-                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                        cudaSuccess)
-    return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  // one CTA: a warp for every 32 slots (in eights, as the scan takes them), and the scans' threads
-  cfg.blockDim = dim3(ctas > 1 ? kSortThreads
-                               : std::min(kSortThreads, std::max(256, (n + 255) / 256 * 256)));
-  cfg.dynamicSmemBytes = sizeof(SortShared);
-  set_dyn_smem((const void *)sort_tokens_kernel, (int)sizeof(SortShared));
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, sort_tokens_kernel, n, n_experts, ids, offsets, perm, slot_pos) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  // 65,536 slots: 10.0 us with eight CTAs, 8.4 with sixteen; 262,144: 27.9 and 17.7
+  const int e = sort_launch(n, [&](int ctas) {
+    const void *kernel = (const void *)sort_tokens_kernel;
+    cudaError_t r = cudaSuccess;
+    if (ctas == 16)
+      r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    // one CTA: a warp for every 32 slots (in eights, as the scan takes them), and the scans' threads
+    cfg.blockDim = dim3(ctas > 1 ? kSortThreads
+                                 : std::min(kSortThreads, std::max(256, (n + 255) / 256 * 256)));
+    cfg.dynamicSmemBytes = sizeof(SortShared);
+    set_dyn_smem(kernel, (int)sizeof(SortShared));
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (r == cudaSuccess)
+      r = cudaLaunchKernelEx(&cfg, sort_tokens_kernel, n, n_experts, ids, offsets, perm, slot_pos);
+    if (r != cudaSuccess) cudaGetLastError();  // not the next launch's error
+    return (int)r;
+  });
+  return e == 0 && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_dispatch_rows(int T, int k, int n_experts, int H, moe_dtype dtype, const void *x, long ldx,

@@ -55,3 +55,26 @@ def test_the_products_plan_asks_through_them():
     body = body[:body.index("\n}\n")]
     assert "static DeviceAnswers" in body and "known.get(dev, split," in body
     assert "std::atomic" not in src
+
+
+@pytest.mark.parametrize("n,refused,tried,status", [
+    (1, 99, "1", 0), (2048, 99, "1", 0), (2049, 99, "8", 0), (32768, 99, "8", 0),
+    (32769, 99, "16", 0), (1048560, 99, "16", 0),
+    (1048560, 16, "16 8", 0),        # no room for sixteen CTAs: eight
+    (1048560, 8, "16 8", 7), (4096, 8, "8", 7), (1, 1, "1", 7)])
+def test_sort_falls_back_to_eight_ctas(tmp_path, n, refused, tried, status):
+    """Launches of `refused` CTAs or more fail."""
+    out = run_cpp(tmp_path, f"""
+  const int e = moe::sort_launch({n}, [](int ctas) {{
+    printf("%d ", ctas);
+    return ctas >= {refused} ? 7 : 0;
+  }});
+  printf("%d", e);""")
+    assert out == tried.split() + [str(status)]
+
+
+def test_the_sort_launches_through_it():
+    with open(os.path.join(CSRC, "tokens.cu")) as f:
+        src = f.read()
+    assert src.count("sort_launch(n, [&](int ctas)") == 1
+    assert src.count("cudaLaunchKernelEx(&cfg, sort_tokens_kernel") == 1
