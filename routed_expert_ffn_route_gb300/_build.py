@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
-PY_EXT = os.path.join(HERE, "_tokens_native.so")  # Python entry points of the token operators
+# Python entry points of the token operators, for this interpreter (its ABI is in the name)
+PY_EXT = os.path.join(HERE, "_tokens_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -74,6 +75,13 @@ def build(force: bool = False, extra=()) -> str:
     return LIB
 
 
+def _entries_key(cmd) -> str:
+    """What the entry points' object was made by and for: an interpreter, a torch, a command.
+    File times do not say it: another environment's torch may be older than the object."""
+    import torch
+    return "\n".join([sys.version, str(torch.__version__), str(torch.version.cuda), *cmd])
+
+
 def _entries_obj(force: bool):
     """Compile the token operators' Python entry points (torch's headers, a host compiler).
     None without torch: the C library needs none, and tokens.py cannot be imported then."""
@@ -83,22 +91,29 @@ def _entries_obj(force: bool):
         return None
     src = os.path.join(CSRC, "tokens_py.cpp")
     obj = os.path.join(OUT_DIR, "tokens_py.o")
-    dep = max(os.path.getmtime(p) for p in [src, torch.__file__] + _headers())
-    if os.path.exists(obj) and os.path.getmtime(obj) >= dep and not force:
-        return obj
     base = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     abi = int(torch.compiled_with_cxx11_abi())
     inc = [base, os.path.join(base, "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], cuda]
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *(a for i in inc for a in ("-isystem", i)),
-           "-c", src, "-o", obj]
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", f'-DTOKENS_TORCH="{torch.__version__}"',
+           *(a for i in inc for a in ("-isystem", i)), "-c", src, "-o", obj]
+    key, made = _entries_key(cmd), obj + ".key"
+    dep = max(os.path.getmtime(p) for p in [src, torch.__file__] + _headers())
+    if os.path.exists(obj) and os.path.exists(made) and not force:
+        with open(made) as f:
+            if f.read() == key and os.path.getmtime(obj) >= dep:
+                return obj
+    if os.path.exists(made):
+        os.remove(made)  # written again once the object stands
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for tokens_py.cpp:\n{r.stderr}")
     if r.stderr.strip():
         sys.stderr.write(r.stderr)
+    with open(made, "w") as f:
+        f.write(key)
     return obj
 
 
@@ -106,6 +121,9 @@ def _link_entries(obj, force: bool):
     """The extension module beside the library it calls; torch's libraries are loaded by torch."""
     if obj is None:
         return
+    untagged = os.path.join(HERE, "_tokens_native.so")  # any interpreter would load it
+    if os.path.exists(untagged) and untagged != PY_EXT:
+        os.remove(untagged)
     if (os.path.exists(PY_EXT) and not force
             and os.path.getmtime(PY_EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
         return

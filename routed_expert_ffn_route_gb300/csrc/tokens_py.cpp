@@ -425,4 +425,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens_native", nullptr, -1, meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tokens_native(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tokens_native(void) {
+  PyObject *m = PyModule_Create(&module);
+  if (m) PyModule_AddStringConstant(m, "torch_version", TOKENS_TORCH);
+  return m;
+}

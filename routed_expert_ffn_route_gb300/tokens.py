@@ -14,11 +14,21 @@ call of the norm where that took 7.3.
 """
 from __future__ import annotations
 
-import torch  # noqa: F401 (its libraries are the extension module's)
+import torch  # (its libraries are the extension module's)
 
 from . import MOE_OK, MoEError, lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
+
+
+def _made_for_this_torch(module):
+    """The extension module, unless it was compiled against another torch's headers."""
+    made_for = getattr(module, "torch_version", "another version")
+    if made_for != str(torch.__version__):
+        raise ImportError(f"the token operators' entry points were built for torch "
+                          f"{made_for}, this is {torch.__version__}: build again "
+                          "(routed_expert_ffn_route_gb300.build())")
+    return module
 
 
 class _Late:
@@ -29,7 +39,7 @@ class _Late:
         global _native
         lib()
         from . import _tokens_native
-        _native = _tokens_native
+        _native = _made_for_this_torch(_tokens_native)
         return getattr(_native, name)
 
 

@@ -57,3 +57,68 @@ def test_every_entry_point_calls_through_the_device_guard():
 def test_a_torch_stream_says_its_device():
     """handle() reads these two attributes of torch.cuda.Stream."""
     assert hasattr(torch.cuda.Stream, "device_index") and hasattr(torch.cuda.Stream, "cuda_stream")
+
+
+# ---------------------------------------------------------- the extension module's versions
+@pytest.fixture
+def build_dir(tmp_path, monkeypatch):
+    """The build module on an empty folder, its compiler calls recorded (each makes its output)."""
+    from routed_expert_ffn_route_gb300 import _build
+    ran = []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("x")
+        return Done
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    monkeypatch.setattr(_build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(_build, "HERE", str(tmp_path))
+    monkeypatch.setattr(_build, "PY_EXT", str(tmp_path / os.path.basename(_build.PY_EXT)))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "libmoe_gb300.so"))
+    (tmp_path / "libmoe_gb300.so").write_text("x")
+    monkeypatch.setattr(_build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    return _build, ran, tmp_path
+
+
+def test_the_object_is_made_again_for_another_torch_or_python(build_dir, monkeypatch):
+    """Also when the other torch's files are older than the object."""
+    build, ran, _ = build_dir
+    obj = build._entries_obj(False)
+    assert len(ran) == 1 and build._entries_obj(False) == obj and len(ran) == 1
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0+other")
+        assert build._entries_obj(False) == obj and len(ran) == 2
+        assert build._entries_obj(False) == obj and len(ran) == 2
+    assert build._entries_obj(False) == obj and len(ran) == 3
+    with monkeypatch.context() as m:
+        m.setattr(build.sys, "version", "3.99.0 (another)")
+        assert build._entries_obj(False) == obj and len(ran) == 4
+
+
+def test_the_module_carries_the_interpreters_abi(build_dir):
+    build, ran, folder = build_dir
+    import importlib.machinery
+    import sysconfig
+    assert build.PY_EXT.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert importlib.machinery.EXTENSION_SUFFIXES[0] == sysconfig.get_config_var("EXT_SUFFIX")
+    old = folder / "_tokens_native.so"  # a module without a tag, which any interpreter loads
+    old.write_text("x")
+    build._link_entries(build._entries_obj(False), False)
+    assert not old.exists() and os.path.exists(build.PY_EXT)
+
+
+def test_a_module_of_another_torch_is_refused(native):
+    from routed_expert_ffn_route_gb300 import tokens
+    assert native.torch_version == str(torch.__version__)
+    assert tokens._made_for_this_torch(native) is native
+
+    class Other:
+        torch_version = "2.0.0+other"
+
+    with pytest.raises(ImportError, match="2.0.0"):
+        tokens._made_for_this_torch(Other)
