@@ -84,10 +84,14 @@ def _entries_key(cmd) -> str:
 
 def _entries_obj(force: bool):
     """Compile the token operators' Python entry points (torch's headers, a host compiler).
-    None without torch: the C library needs none, and tokens.py cannot be imported then."""
+    None where they cannot be had, without torch, with a torch without CUDA or without Python's
+    headers: the C library needs none of these, and a call of a token operator says so then."""
     try:
         import torch
     except ImportError:
+        return None
+    if torch.version.cuda is None or not os.path.exists(
+            os.path.join(sysconfig.get_paths()["include"], "Python.h")):
         return None
     src = os.path.join(CSRC, "tokens_py.cpp")
     obj = os.path.join(OUT_DIR, "tokens_py.o")

@@ -38,7 +38,12 @@ class _Late:
     def __getattr__(self, name):
         global _native
         lib()
-        from . import _tokens_native
+        try:
+            from . import _tokens_native
+        except ImportError as e:
+            raise ImportError("the token operators' entry points have not been built for this "
+                              "Python: build() makes them where torch has CUDA and Python's "
+                              "headers are installed") from e
         _native = _made_for_this_torch(_tokens_native)
         return getattr(_native, name)
 

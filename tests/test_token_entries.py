@@ -122,3 +122,30 @@ def test_a_module_of_another_torch_is_refused(native):
 
     with pytest.raises(ImportError, match="2.0.0"):
         tokens._made_for_this_torch(Other)
+
+
+def test_the_library_builds_where_the_module_cannot(build_dir, monkeypatch):
+    """A torch without CUDA, or a Python without headers, is no reason to fail: the C library needs
+    neither."""
+    build, ran, folder = build_dir
+    with monkeypatch.context() as m:
+        m.setattr(torch.version, "cuda", None)
+        assert build._entries_obj(False) is None
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_paths", lambda: {"include": str(folder)})
+        assert build._entries_obj(False) is None
+    assert not ran
+    build._link_entries(None, False)
+    assert not ran
+
+
+def test_a_call_without_the_module_says_so(native, monkeypatch):
+    import sys
+
+    from routed_expert_ffn_route_gb300 import tokens
+    monkeypatch.setattr(tokens, "_native", tokens._Late())
+    monkeypatch.delattr(moe, "_tokens_native", raising=False)
+    monkeypatch.setitem(sys.modules, "routed_expert_ffn_route_gb300._tokens_native", None)
+    x = torch.zeros(2, 2, dtype=torch.int32)
+    with pytest.raises(ImportError, match="have not been built"):
+        moe.moe_sort_tokens(x, 1, x, x, x)
