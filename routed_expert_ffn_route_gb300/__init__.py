@@ -9,6 +9,7 @@ Names mirror the C entry points (moe_pack_weights, moe_route_topk, moe_layer_for
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 import threading
 
@@ -19,8 +20,7 @@ __all__ = [
     "moe_unpack_weights", "moe_route_topk", "moe_layer_forward", "moe_read_status",
     "moe_debug_permutation", "moe_q8_0_quantize", "moe_debug_block_dots",
     "moe_debug_wait_timeout", "moe_layer_forward_experts", "moe_layer_forward_next",
-    "moe_rmsnorm_e4m3", "moe_sort_tokens", "moe_dispatch_rows", "moe_dispatch_rows_grad",
-    "moe_combine_rows", "moe_combine_rows_grad", "moe_linear", "ACTIVATIONS", "EXPORTED",
+    "EXPORTED",
     "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_WORKSPACE",
     "MOE_ERR_CUDA", "MOE_ERR_TIMEOUT", "MOE_ERR_NUMERIC", "MOE_ERR_PACKED",
 ]
@@ -48,6 +48,8 @@ EXPORTED = [
 _TOKEN_OPERATORS = ("moe_rmsnorm_e4m3", "moe_sort_tokens", "moe_dispatch_rows",
                     "moe_dispatch_rows_grad", "moe_combine_rows", "moe_combine_rows_grad",
                     "moe_linear", "ACTIVATIONS")
+if importlib.util.find_spec("torch") is not None:  # the rest of the package imports without it
+    __all__ += _TOKEN_OPERATORS
 
 # stages bracketed by the events of moe_layer_forward_timed
 STAGES = ["router", "permute", "act_encode", "gate_up", "down", "combine"]

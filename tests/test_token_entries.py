@@ -149,3 +149,16 @@ def test_a_call_without_the_module_says_so(native, monkeypatch):
     x = torch.zeros(2, 2, dtype=torch.int32)
     with pytest.raises(ImportError, match="have not been built"):
         moe.moe_sort_tokens(x, 1, x, x, x)
+
+
+@pytest.mark.parametrize("torch_there", [True, False])
+def test_star_import_does_not_need_torch(torch_there):
+    """The binding of the packed layer imports without torch; the token operators need it."""
+    import subprocess
+    import sys
+    code = ("import sys\n" + ("" if torch_there else "sys.modules['torch'] = None\n")
+            + "from routed_expert_ffn_route_gb300 import *\n"
+              "assert callable(moe_layer_forward) and callable(make_config)\n"
+              f"assert ('moe_linear' in globals()) == {torch_there}\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
