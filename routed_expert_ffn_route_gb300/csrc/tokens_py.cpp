@@ -10,6 +10,7 @@
 // wrong types TypeError.  They are private: tokens.py documents them.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -128,6 +129,7 @@ struct Told {
 // The operands of one call: all on one CUDA device.
 struct Call {
   int dev;
+  c10::SmallVector<const at::Tensor *, 4> written;
   explicit Call(const at::Tensor &first) : dev(first.is_cuda() ? first.get_device() : -1) {}
 
   void check(const at::Tensor &t, const char *name, at::ScalarType type,
@@ -174,10 +176,34 @@ struct Call {
                      std::initializer_list<int64_t> shape) const {
     return o == Py_None ? nullptr : flat(o, name, type, shape);
   }
+  // The same for a tensor that the call writes.  Autograd does not see the call: a tensor that is
+  // part of a graph may not be written while graphs are recorded, and the others' version counters
+  // move on, so that a backward pass finds out when a tensor that it saved has been overwritten.
+  void writes(PyObject *o, const char *name) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.requires_grad() && at::GradMode::is_enabled())
+      raise(PyExc_ValueError, std::string(name) + " requires a gradient, and autograd does not "
+                              "record the call: write it under torch.no_grad()");
+    written.push_back(&t);
+  }
+  void *out_rows(PyObject *o, const char *name, at::ScalarType type, int64_t n, int64_t width,
+                 long &ld) {
+    writes(o, name);
+    return rows(o, name, type, n, width, ld);
+  }
+  void *out_flat(PyObject *o, const char *name, at::ScalarType type,
+                 std::initializer_list<int64_t> shape) {
+    writes(o, name);
+    return flat(o, name, type, shape);
+  }
   // body(stream) on the operands' device
   template <typename F>
   long launch(PyObject *stream, F body) const {
-    return on_device<Cuda>(dev, stream, body);
+    const long status = on_device<Cuda>(dev, stream, body);
+    if (status == MOE_OK)
+      for (const at::Tensor *t : written)
+        if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+    return status;
   }
 };
 
@@ -213,7 +239,7 @@ PyObject *run(Py_ssize_t n, Py_ssize_t want, F body) {
 PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 10, [&]() {
     const at::Tensor &x = tensor(a[0], "x");
-    const Call c(x);
+    Call c(x);
     const int64_t T = dim(x, "x", 2, 0), H = x.size(1);
     const at::ScalarType dt = x.scalar_type();
     const int group = number32(a[7], "group"), normalize = PyObject_IsTrue(a[8]);
@@ -221,12 +247,13 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (PyErr_Occurred()) throw Raised{};
     long ldx, ldq, lda, ldr;
     const void *px = c.rows(a[0], "x", dt, T, H, ldx);
-    uint8_t *pq = (uint8_t *)c.rows(a[1], "q", at::kFloat8_e4m3fn, T, H, ldq);
-    float *ps = (float *)c.flat(a[2], "scale", at::kFloat,
-                                {T, group > 0 ? (H + group - 1) / group : 1});
+    uint8_t *pq = (uint8_t *)c.out_rows(a[1], "q", at::kFloat8_e4m3fn, T, H, ldq);
+    float *ps = (float *)c.out_flat(a[2], "scale", at::kFloat,
+                                    {T, group > 0 ? (H + group - 1) / group : 1});
     const void *pa = c.rows_or_null(a[3], "add", dt, T, H, lda);
     const void *pw = c.flat_or_null(a[4], "weight", dt, {H});
-    void *pr = c.rows_or_null(a[5], "resid", dt, T, H, ldr);
+    ldr = 0;
+    void *pr = a[5] == Py_None ? nullptr : c.out_rows(a[5], "resid", dt, T, H, ldr);
     const int rt = row_type(dt);
     const int t32 = size32(T, "x"), h32 = size32(H, "x");
     return c.launch(a[9], [&](void *st) {
@@ -240,12 +267,12 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *sort(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 6, [&]() {
     const at::Tensor &ids = tensor(a[0], "ids");
-    const Call c(ids);
+    Call c(ids);
     const int64_t T = dim(ids, "ids", 2, 0), k = ids.size(1), E = number(a[1]);
     const int32_t *pi = (const int32_t *)c.flat(a[0], "ids", at::kInt, {T, k});
-    int32_t *po = (int32_t *)c.flat(a[2], "offsets", at::kInt, {E + 1});
-    int32_t *pp = (int32_t *)c.flat(a[3], "perm", at::kInt, {T * k});
-    int32_t *ps = (int32_t *)c.flat(a[4], "slot_pos", at::kInt, {T, k});
+    int32_t *po = (int32_t *)c.out_flat(a[2], "offsets", at::kInt, {E + 1});
+    int32_t *pp = (int32_t *)c.out_flat(a[3], "perm", at::kInt, {T * k});
+    int32_t *ps = (int32_t *)c.out_flat(a[4], "slot_pos", at::kInt, {T, k});
     const int t32 = size32(T, "ids"), k32 = size32(k, "ids"), e32 = size32(E, "n_experts");
     return c.launch(a[5], [&](void *st) {
       return moe_sort_tokens(t32, k32, e32, pi, po, pp, ps, st);
@@ -257,7 +284,7 @@ PyObject *sort(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 7, [&]() {
     const at::Tensor &x = tensor(a[0], "x");
-    const Call c(x);
+    Call c(x);
     const int64_t T = dim(x, "x", 2, 0), H = x.size(1);
     const int64_t k = dim(tensor(a[1], "slot_pos"), "slot_pos", 2, 1);
     const int64_t E1 = dim(tensor(a[2], "offsets"), "offsets", 1, 0);
@@ -266,7 +293,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const void *px = c.rows(a[0], "x", dt, T, H, ldx);
     const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
     const int32_t *po = (const int32_t *)c.flat(a[2], "offsets", at::kInt, {E1});
-    void *pxs = c.flat(a[3], "xs", dt, {T * k, H});
+    void *pxs = c.out_flat(a[3], "xs", dt, {T * k, H});
     int64_t S = 0;
     const float *psc = nullptr;
     float *pss = nullptr;
@@ -274,7 +301,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
       S = dim(tensor(a[4], "scale"), "scale", 2, 1);
       psc = (const float *)c.rows(a[4], "scale", at::kFloat, T, S, ldsc);
       if (a[5] == Py_None) raise(PyExc_ValueError, "scale_s is needed with scale");
-      pss = (float *)c.flat(a[5], "scale_s", at::kFloat, {T * k, S});
+      pss = (float *)c.out_flat(a[5], "scale_s", at::kFloat, {T * k, S});
     }
     const int rt = row_type(dt), t32 = size32(T, "x"), k32 = size32(k, "slot_pos");
     const int h32 = size32(H, "x"), s32 = size32(S, "scale"), e32 = size32(E1 - 1, "offsets");
@@ -290,13 +317,13 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 6, [&]() {
     const at::Tensor &y = tensor(a[0], "y"), &pos = tensor(a[1], "slot_pos");
     const at::Tensor &out = tensor(a[2], "out");
-    const Call c(y);
+    Call c(y);
     const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(out, "out", 2, 1);
     const at::ScalarType yt = y.scalar_type(), ot = out.scalar_type();
     long ldo, lda;
     const void *py = c.flat(a[0], "y", yt, {T * k, H});
     const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
-    void *po = c.rows(a[2], "out", ot, T, H, ldo);
+    void *po = c.out_rows(a[2], "out", ot, T, H, ldo);
     const float *pw = (const float *)c.flat_or_null(a[3], "w", at::kFloat, {T, k});
     const void *pa = c.rows_or_null(a[4], "add", ot, T, H, lda);
     const int ry = row_type(yt), ro = row_type(ot), t32 = size32(T, "slot_pos");
@@ -312,7 +339,7 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 8, [&]() {
     const at::Tensor &dout = tensor(a[0], "dout"), &pos = tensor(a[2], "slot_pos");
-    const Call c(dout);
+    Call c(dout);
     const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(dout, "dout", 2, 1);
     const int64_t E1 = dim(tensor(a[3], "offsets"), "offsets", 1, 0);
     const at::ScalarType dt = dout.scalar_type();
@@ -322,8 +349,8 @@ PyObject *combine_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int32_t *pp = (const int32_t *)c.flat(a[2], "slot_pos", at::kInt, {T, k});
     const int32_t *po = (const int32_t *)c.flat(a[3], "offsets", at::kInt, {E1});
     const float *pw = (const float *)c.flat_or_null(a[4], "w", at::kFloat, {T, k});
-    void *pdy = c.flat(a[5], "dy", dt, {T * k, H});
-    float *pdw = (float *)c.flat(a[6], "dw", at::kFloat, {T, k});
+    void *pdy = c.out_flat(a[5], "dy", dt, {T * k, H});
+    float *pdw = (float *)c.out_flat(a[6], "dw", at::kFloat, {T, k});
     const int rt = row_type(dt), t32 = size32(T, "slot_pos"), k32 = size32(k, "slot_pos");
     const int h32 = size32(H, "dout"), e32 = size32(E1 - 1, "offsets");
     return c.launch(a[7], [&](void *st) {
@@ -338,13 +365,13 @@ PyObject *dispatch_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 4, [&]() {
     const at::Tensor &dxs = tensor(a[0], "dxs"), &pos = tensor(a[1], "slot_pos");
     const at::Tensor &dx = tensor(a[2], "dx");
-    const Call c(dxs);
+    Call c(dxs);
     const int64_t T = dim(pos, "slot_pos", 2, 0), k = pos.size(1), H = dim(dx, "dx", 2, 1);
     const at::ScalarType dt = dxs.scalar_type(), xt = dx.scalar_type();
     long ldx;
     const void *pd = c.flat(a[0], "dxs", dt, {T * k, H});
     const int32_t *pp = (const int32_t *)c.flat(a[1], "slot_pos", at::kInt, {T, k});
-    void *px = c.rows(a[2], "dx", xt, T, H, ldx);
+    void *px = c.out_rows(a[2], "dx", xt, T, H, ldx);
     const int rd = row_type(dt), rx = row_type(xt), t32 = size32(T, "slot_pos");
     const int k32 = size32(k, "slot_pos"), h32 = size32(H, "dx");
     return c.launch(a[3], [&](void *st) {
@@ -358,7 +385,7 @@ PyObject *dispatch_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return run(n, 11, [&]() {
     const at::Tensor &x = tensor(a[0], "x"), &out = tensor(a[2], "out");
-    const Call c(x);
+    Call c(x);
     const int64_t R = dim(x, "x", 2, 0), K = x.size(1), N = dim(out, "out", 2, 1);
     const at::ScalarType dt = x.scalar_type(), ot = out.scalar_type();
     const int act = number32(a[6], "act");
@@ -374,7 +401,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     long ldx, ldo, ldr;
     const void *px = c.rows(a[0], "x", dt, R, K, ldx);
     const void *pw = dense ? c.flat(a[1], "w", dt, {rows, K}) : c.flat(a[1], "w", dt, {E, rows, K});
-    void *pout = c.rows(a[2], "out", ot, R, N, ldo);
+    void *pout = c.out_rows(a[2], "out", ot, R, N, ldo);
     const float *pxs = nullptr;
     if (a[3] != Py_None)
       pxs = (const float *)(tensor(a[3], "x_scale").dim() == 1
@@ -386,7 +413,8 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     };
     const float *pws = per_row(a[4], "w_scale"), *pb = per_row(a[5], "bias");
     const void *pr = c.rows_or_null(a[7], "residual", ot, R, N, ldr);
-    int32_t *pst = (int32_t *)c.flat_or_null(a[9], "status", at::kInt, {1});
+    int32_t *pst = nullptr;
+    if (a[9] != Py_None) pst = (int32_t *)c.out_flat(a[9], "status", at::kInt, {1});
     const int rt = row_type(dt), ro = row_type(ot), r32 = size32(R, "x"), n32 = size32(N, "out");
     const int k32 = size32(K, "x"), e32 = size32(E, "offsets");
     return c.launch(a[10], [&](void *st) {
@@ -419,7 +447,8 @@ PyObject *trace(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(rmsnorm),      METHOD(sort),          METHOD(dispatch),
                          METHOD(combine),      METHOD(combine_grad),  METHOD(dispatch_grad),
-                         METHOD(linear),       METHOD(trace),         {nullptr, nullptr, 0, nullptr}};
+                         METHOD(linear),       METHOD(trace),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens_native", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -8,6 +8,11 @@ every call may be captured into a graph.  Shapes, types, strides and devices are
 C entry points see only addresses): a wrong one raises ValueError or TypeError, an error of the
 C entry point MoEError.
 
+The calls stand outside autograd, as the rest of the package does: they record no graph, whatever
+their operands require, so a model that trains through them makes them in the forward and backward
+of a torch.autograd.Function.  What they write counts as written: version counters move on, and an
+output that requires a gradient is refused while graphs are recorded.
+
 At decode sizes the host side of a call counts as much as its kernel, so tensors are read and
 checked by a small extension module (csrc/tokens_py.cpp) and not through ctypes: 2.7 us for a whole
 call of the norm where that took 7.3.

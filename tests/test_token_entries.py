@@ -162,3 +162,51 @@ def test_star_import_does_not_need_torch(torch_there):
               f"assert ('moe_linear' in globals()) == {torch_there}\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+# ------------------------------------------------------------------------------ autograd
+def zeros(*shape, dtype=torch.bfloat16, grad=False):
+    return torch.zeros(*shape, dtype=dtype, requires_grad=grad)
+
+
+OUTPUTS = ["q_scale", "resid", "xs", "scale_s", "combined", "dy", "dw", "dx", "product"]
+
+
+def write(which):
+    """A call whose output `which` requires a gradient (on the host: other checks come later)."""
+    g = {n: n == which for n in OUTPUTS}
+    T, k, H, f32 = 4, 2, 64, torch.float32
+    x, pos = zeros(T, H), torch.zeros(T, k, dtype=torch.int32)
+    off, xs = torch.zeros(9, dtype=torch.int32), zeros(T * k, H)
+    w = zeros(T, k, dtype=f32)
+    if which in ("q_scale", "resid"):
+        moe.moe_rmsnorm_e4m3(x, torch.zeros(T, H, dtype=torch.float8_e4m3fn),
+                             zeros(T, 1, dtype=f32, grad=g["q_scale"]),
+                             resid=zeros(T, H, grad=g["resid"]))
+    elif which in ("xs", "scale_s"):
+        moe.moe_dispatch_rows(x, pos, off, zeros(T * k, H, grad=g["xs"]),
+                              scale=zeros(T, 1, dtype=f32),
+                              scale_s=zeros(T * k, 1, dtype=f32, grad=g["scale_s"]))
+    elif which == "combined":
+        moe.moe_combine_rows(xs, pos, zeros(T, H, grad=True), w=w)
+    elif which in ("dy", "dw"):
+        moe.moe_combine_rows_grad(x, xs, pos, off, w, zeros(T * k, H, grad=g["dy"]),
+                                  zeros(T, k, dtype=f32, grad=g["dw"]))
+    elif which == "dx":
+        moe.moe_dispatch_rows_grad(xs, pos, zeros(T, H, grad=True))
+    else:
+        moe.moe_linear(x, zeros(32, H), zeros(T, 32, grad=True))
+
+
+@pytest.mark.parametrize("which", OUTPUTS)
+def test_an_output_in_a_recorded_graph_is_refused(native, which):
+    with pytest.raises(ValueError, match="requires a gradient"):
+        write(which)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+        write(which)  # passes that check
+
+
+def test_inputs_that_require_gradients_are_taken(native):
+    x, pos = zeros(8, 64, grad=True), torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        moe.moe_combine_rows(x, pos, zeros(4, 64), w=zeros(4, 2, dtype=torch.float32, grad=True))
