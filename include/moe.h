@@ -361,10 +361,10 @@ int moe_dispatch_rows_grad(int T, int k, int H, moe_dtype dtype, const void *dxs
  * expert get zeros and are not read.  act = SWIGLU: w has 2 N rows per expert (gate rows, then
  * up rows; w_scale and bias too) and out = silu(z_gate) * z_up + residual.
  * Accumulation is fp32 on the tensor cores, whose sums are truncated; for F32 outputs they are
- * added up in registers every few hundred of K, rounded to nearest.  x, w and x's rows 16-byte aligned; K a multiple
- * of 16, N of 16 for SWIGLU, E <= 256, else MOE_ERR_UNSUPPORTED.  status: optional device
- * int32, set to MOE_ERR_TIMEOUT if a bounded wait gave up (the output is then undefined), else
- * left as it is. */
+ * added up in registers every few hundred of K, rounded to nearest.  x, w and (R > 1) x's rows
+ * 16-byte aligned; K a multiple of 16, N of 16 for SWIGLU, E <= 256, else MOE_ERR_UNSUPPORTED.
+ * status: optional device int32, set to MOE_ERR_TIMEOUT if a bounded wait gave up (the output is
+ * then undefined), else left as it is. */
 int moe_linear(int R, int N, int K, int n_experts, const void *x, long ldx, moe_dtype dtype,
                const float *x_scale, const void *w, const float *w_scale, const float *bias,
                moe_act act, const void *residual, long ldres, const int32_t *offsets, void *out,

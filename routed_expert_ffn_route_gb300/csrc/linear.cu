@@ -1187,6 +1187,7 @@ static int linear_call(int R, int N, int K, int n_experts, const void *x, long l
       (n_experts && !offsets))
     return MOE_ERR_INVALID_ARG;
   const uintptr_t eo = out_dtype == MOE_DT_F32 ? 4 : 2;
+  if (R == 1) ldx = K;  // there is no next row for the distance to lead to
   if ((uintptr_t)x % 16 || (uintptr_t)w % 16 || (uintptr_t)(ldx * es) % 16 ||
       ((uintptr_t)out | (uintptr_t)residual) % eo ||
       ((uintptr_t)x_scale | (uintptr_t)w_scale | (uintptr_t)bias | (uintptr_t)offsets |
