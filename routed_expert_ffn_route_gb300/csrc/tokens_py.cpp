@@ -104,7 +104,12 @@ long on_device(int dev, PyObject *stream, F body) {
 }
 
 struct Cuda {
-  using Guard = c10::cuda::CUDAGuard;
+  struct Guard {  // one look at the current device where it is the right one
+    c10::cuda::OptionalCUDAGuard g;
+    explicit Guard(c10::DeviceIndex dev) {
+      if (c10::cuda::current_device() != dev) g.set_index(dev);
+    }
+  };
   static void *current(int dev) {
     return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
   }

@@ -51,7 +51,7 @@ def test_every_entry_point_calls_through_the_device_guard():
     calls = re.findall(r"return (moe_\w+)\(", src)
     launched = re.findall(r"c\.launch\(a\[\d+\], \[&\]\(void \*st\) \{\s*return (moe_\w+)\(", src)
     assert sorted(calls) == sorted(launched) and len(calls) == 7
-    assert "on_device<Cuda>" in src and "using Guard = c10::cuda::CUDAGuard;" in src
+    assert "on_device<Cuda>" in src and "c10::cuda::OptionalCUDAGuard g;" in src
 
 
 def test_a_torch_stream_says_its_device():
