@@ -66,8 +66,8 @@ struct Unlocked {
 };
 
 // an attribute of a stream object as a Python integer; null where there is none and it may be so
-PyObject *attribute(PyObject *o, const char *name, bool needed) {
-  PyObject *v = PyObject_GetAttrString(o, name);
+PyObject *attribute(PyObject *o, PyObject *name, bool needed) {
+  PyObject *v = PyObject_GetAttr(o, name);
   if (v) return v;
   if (needed || !PyErr_ExceptionMatches(PyExc_AttributeError)) throw Raised{};
   PyErr_Clear();
@@ -76,7 +76,9 @@ PyObject *attribute(PyObject *o, const char *name, bool needed) {
 
 // the handle of a torch.cuda.Stream, which must be one of device `dev`
 void *handle(PyObject *stream, int dev) {
-  if (PyObject *d = attribute(stream, "device_index", false)) {
+  static PyObject *device_index = PyUnicode_InternFromString("device_index");
+  static PyObject *cuda_stream = PyUnicode_InternFromString("cuda_stream");
+  if (PyObject *d = attribute(stream, device_index, false)) {
     const long on = PyLong_AsLong(d);
     Py_DECREF(d);
     if (on == -1 && PyErr_Occurred()) throw Raised{};
@@ -84,7 +86,7 @@ void *handle(PyObject *stream, int dev) {
       raise(PyExc_ValueError, "the stream is on device " + std::to_string(on) +
                                   ", the operands are on device " + std::to_string(dev));
   }
-  PyObject *h = attribute(stream, "cuda_stream", true);
+  PyObject *h = attribute(stream, cuda_stream, true);
   void *s = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
   if (PyErr_Occurred()) throw Raised{};
