@@ -55,7 +55,8 @@ std::string text(std::initializer_list<int64_t> shape) {
 
 // a 32-bit size of the C interface
 int size32(int64_t v, const char *name) {
-  if (v > 2147483647) raise(PyExc_ValueError, std::string(name) + " is too large");
+  if (v > 2147483647 || v < -2147483647 - 1)
+    raise(PyExc_ValueError, std::string(name) + " is out of range: " + std::to_string(v));
   return (int)v;
 }
 

@@ -210,3 +210,12 @@ def test_inputs_that_require_gradients_are_taken(native):
     x, pos = zeros(8, 64, grad=True), torch.zeros(4, 2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA device"):
         moe.moe_combine_rows(x, pos, zeros(4, 64), w=zeros(4, 2, dtype=torch.float32, grad=True))
+
+
+# ------------------------------------------------------------------------ 32-bit numbers
+@pytest.mark.parametrize("group", [-2 ** 32, 2 ** 32, -2 ** 31 - 1, 2 ** 31, -2 ** 40 + 128])
+def test_numbers_beyond_32_bits_are_refused(native, group):
+    """A group of -2^32 is not one of 0."""
+    x, q = zeros(4, 256), torch.zeros(4, 256, dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="group is out of range"):
+        moe.moe_rmsnorm_e4m3(x, q, zeros(4, 1, dtype=torch.float32), group=group)
