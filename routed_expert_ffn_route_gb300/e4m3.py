@@ -1,13 +1,16 @@
 """A MoE layer whose experts are e4m3 weights with row scales, on the token operators.
 
-The packed layer (`moe_layer_forward`) takes integer experts; this is the same layer for
-experts that are kept as 8-bit floating-point rows, routed by the same router:
+The packed layer (`moe_layer_forward`) takes integer experts; this is the routed part of such a
+layer (no shared expert) for experts that are kept as 8-bit floating-point rows:
 
     r   = resid + add                                   (the residual stream, in its own type)
     x   = RMSNorm(r) * norm_weight as e4m3 rows with a scale each
-    ids, w = the router's experts and weights of each token (moe_route_topk, or the caller's)
     h   = silu(x_s Wg_e^T) * (x_s Wu_e^T) on the rows sorted by expert, again as e4m3 rows
     out = r + sum_j w[t, j] * (h Wd_e^T)[row of (t, j)]
+
+The experts and weights of each token come from outside: from moe_route_topk, or any other router.
+A router wants the normalised hidden states in fp32 or bf16 before forward() runs, which the caller
+computes (x here is 8-bit rows and scales only).
 
 Every step runs in the library's kernels on buffers that this object owns, so that a step can
 be captured in a CUDA graph.  What the device finds out on the way (a bounded wait that gave up:
@@ -62,7 +65,7 @@ class E4m3Experts:
 
     def forward(self, resid, add, ids, w):
         """resid [T, H] and add (the attention's output, or None) of the layer's dtype, ids int32
-        and w fp32 [T, k] as moe_route_topk writes them.  Returns the new residual stream, a view
+        and w fp32 [T, k] as moe_route_topk writes them (ids outside [0, E) are left out).  Returns the new residual stream, a view
         of the layer's buffer."""
         T = resid.shape[0]
         if T > self.t_max:
