@@ -307,9 +307,10 @@ int moe_residual_rmsnorm(int T, int H, float *resid, const float *add, const uin
  *   shorter; 0 = the whole row): scale = max|y| / 448, q = e4m3(y * 448 / max|y|), to nearest.
  * x, add, resid [T][H] of dtype (F32, BF16, F16), q [T][H] e4m3 codes, scale
  * [T][ceil(H / group)] fp32, contiguous.  The norm is taken of the rounded r; sums are fp32
- * (squares that overflow fp32 give y = 0).  A group whose largest |y| is below 2^-100 gets
- * scale 0 and codes 0; one that holds a NaN or an infinity gets a NaN or infinite scale.
- * resid may be x or add (same ld).  With normalize = 0 it quantises rows as they are: weights
+ * (squares that overflow fp32 give y = 0, squares below its range count as 0), and r * weight is
+ * formed first, in fp32, so that it has to lie in fp32's range.  A group whose largest |y| is
+ * below 2^-100 gets scale 0 and codes 0; one that holds a NaN or an infinity gets a NaN or
+ * infinite scale.  resid may be x or add (same ld).  With normalize = 0 it quantises rows as they are: weights
  * or hidden activations for moe_linear.  1 <= H <= 32768 (else MOE_ERR_UNSUPPORTED). */
 int moe_rmsnorm_e4m3(int T, int H, const void *x, long ldx, moe_dtype dtype, const void *add,
                      long ldadd, const void *weight, float eps, int normalize, int group,

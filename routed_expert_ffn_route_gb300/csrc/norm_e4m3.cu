@@ -6,8 +6,12 @@
 // The statistics are fp32.  The largest |y| of a group is the largest |r w| times the row's
 // factor, so the sum of squares and the maxima come out of the same single reduction and
 // every element is read from memory once: the row stays in registers between the reduction
-// and the encoding.  Bound by memory: 8192 x 6144 bf16 with a residual moves 352 MB in 55 us, 6.4
-// TB/s of the 6.75 that a copy reaches.
+// and the encoding.  (r w is formed before the row's factor is known, so that it has to lie in
+// fp32's range itself.)  Bound by memory: 8192 x 6144 bf16 with a residual moves 352 MB in 55 us,
+// 6.4 TB/s of the 6.8 that a copy reaches.
+// Rows past 16384 elements are held in eight packs a thread, which do not fit its registers beside
+// the next row's: 16-bit types spill 144 to 324 bytes a thread, fp32 some 700 to 1050, and it
+// shows: 4096 x 28672 bf16 212 us with a residual (3.9 TB/s), 132 us quantised alone (2.7 TB/s).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -230,7 +234,9 @@ static cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
   // Few rows: as many threads as the row has packs, the shortest path through one row.  Many
   // rows: two packs a thread (8192 x 6144 bf16 with residual: one 71 us, two 55, three 75, four
   // 63: fewer leave fewer loads in flight, more take the registers of other rows; fp32, twice
-  // the bytes a pack: one 104 us, two 111).
+  // the bytes a pack: one 104 us, two 111).  Two packs reach 6144 elements with three CTAs an SM;
+  // wider 16-bit rows take four: 8192 x 5120 46 us (6.4 TB/s), 6144 55.5 (6.35), 7168 67 (6.1),
+  // 8192 72 (6.5), 12288 118 (6.0), 16384 142 (6.6).
   const bool one = a.T <= 2 * dev_info().sms || sizeof(T) == 4;
   auto fits = [&](int p) { return threads(p) <= norm_threads(p, sizeof(T)); };
   if (one && fits(1)) return launch_norm_p<T, 1, A>(a, dim3(threads(1)), st);
