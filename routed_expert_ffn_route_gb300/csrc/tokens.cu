@@ -401,7 +401,9 @@ static cudaError_t launch_combine_rows(const CombineArgs &a, cudaStream_t st) {
                       (uintptr_t)(a.ldadd * sizeof(TO)) | (uintptr_t)(a.ldout * sizeof(TO));
   const int acc = access_of(p, a.H, sizeof(TY));
   if (acc == kVec) return launch_combine_v<TY, TO, kVec>(a, st);
-  // the words of a pack are the same elements only where both types have one size
+  // the words of a pack are the same elements only where both types have one size; of two sizes,
+  // rows off 8 elements move one element at a time (16384 x 4 bf16 rows to fp32: of 2048 61 us, of
+  // 2050 198; to bf16 52 and 72, of 2051 179)
   constexpr int W = sizeof(TY) == sizeof(TO) ? kWord : kAny;
   return acc == kWord ? launch_combine_v<TY, TO, W>(a, st) : launch_combine_v<TY, TO, kAny>(a, st);
 }
@@ -517,7 +519,8 @@ int moe_dispatch_rows(int T, int k, int n_experts, int H, moe_dtype dtype, const
   const float *sc = n_scales ? scale : nullptr;
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
-  // the widest unit that every row's start and length allow
+  // the widest unit that every row's start and length allow (16384 x 4 rows: of 2048 e4m3 26 us, of
+  // 2052 29, of 2050 38, of 2051, a byte a lane, 55; of 2048 bf16 51, of 2050 52, of 2051 65)
   if (al % 16 == 0)
     e = launch_dispatch<uint4>(T, k, n_experts, row, ld, x, slot_pos, offsets, xs, n_scales, sc,
                                ldscale, scale_s, st);
