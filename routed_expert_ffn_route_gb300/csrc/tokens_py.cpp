@@ -3,11 +3,11 @@
 // The package's other functions go through ctypes.  A call of a token operator has up to six
 // tensors and twenty arguments; reading the tensors from Python and converting the arguments with
 // ctypes took 5 us, twice the launch, and at decode sizes that is most of the call (7.3 us for a
-// norm of one row, 2.7 this way).  These
-// functions read the tensors through torch's C++ headers, check them, and call the C entry point
-// with the operands' device current, on that device's current stream or a given one, with the
-// interpreter's lock released.  They return its status; wrong shapes and strides raise ValueError,
-// wrong types TypeError.  They are private: tokens.py documents them.
+// norm of one row, 2.3 this way).  These functions read the tensors through torch's C++ headers,
+// check them, and call the C entry point with the operands' device current, on that device's
+// current stream or a given one, with the interpreter's lock released.  They return its status;
+// wrong shapes and strides raise ValueError, wrong types TypeError.  They are private: tokens.py
+// documents them.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/grad_mode.h>
