@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(MODE == kSplit ? 384 : kLinThreads, MODE == kS
   if (PAIR) cluster_sync(); else __syncthreads();  // nobody still uses a peer's barriers
   tc::fence_after_sync();
   if (*abort) {  // the same for all threads: every role has left
-    lin_drain<PAIR>(b, a.stages, rank, warp, lane);
+    lin_drain<PAIR>(b, b->full, a.stages, rank, warp, lane);
     tc::fence_before_sync();
     if (PAIR) cluster_sync(); else __syncthreads();
     tc::fence_after_sync();

@@ -14,18 +14,16 @@
 #include "elem.cuh"
 #include "expert_args.cuh"
 #include "host.cuh"
+#include "linear_plan.cuh"
 #include "moe_internal.cuh"
 #include "tc.cuh"
 
 namespace moe {
 
-constexpr int kLinM = 128;         // weight rows per CTA and tile
 constexpr int kLinMaxN = 256;      // token rows per tile
-constexpr int kLinStages = 12;     // ring slots at most
 constexpr int kLinMaxE = 256;
 constexpr int kLinEpi = 8;         // epilogue warps: two per quarter of the tensor-memory lanes
 constexpr int kLinThreads = 64 + 32 * kLinEpi;
-constexpr int kLinRing = 192 * 1024;  // shared memory of the ring and the exchange, at most
 constexpr int kLinPitch = 36;      // floats per column of a warp's staged chunk (32 features)
 constexpr int kLinStage = kLinEpi * 16 * kLinPitch * 4;  // bytes of the staged chunks
 constexpr long kLinWaitNs = 2000000000L;
@@ -40,20 +38,9 @@ constexpr long kLinLateNs = 50000000L;  // a pair's copies, after a wait gave up
 constexpr int kLinExact = 4;
 template <typename TO>
 constexpr bool lin_exact = sizeof(TO) == 4;
-// columns between the two accumulators, and the largest tiles whose sums fit the registers
+// columns between the two accumulators
 template <typename TO>
 constexpr int kLinAcc = lin_exact<TO> ? 128 : kLinMaxN;
-constexpr int kLinExactN = 128, kLinExactSplitN = 64;
-
-// How CTAs share a tile:
-//   kOne    one CTA a tile, persistent.
-//   kPair   two CTAs (the two SMs of a TPC) a tile of 256 weight rows: each loads its own 128
-//           weight rows and half of the token rows, and the leader issues MMAs of M = 256 that
-//           read both halves, so token rows cross from L2 once for 256 weight rows.
-//   kSplit  a cluster of up to eight CTAs a tile, each over a part of K, not persistent: the
-//           partial sums are exchanged through distributed shared memory and added in rank
-//           order, each CTA finishing a share of the columns.
-enum LinMode { kOne = 0, kPair = 1, kSplit = 2 };
 
 struct LinArgs {
   const float *x_scale, *w_scale, *bias;
@@ -80,7 +67,7 @@ struct alignas(16) LinBars {
   uint64_t full[kLinStages], empty[kLinStages], acc_full[2], acc_empty[2], drain, never;
   uint32_t tmem;
   int abort_flag;
-  uint32_t armed, phases;  // for the drain: stages with a copy started, and their last phase
+  uint32_t armed, phases;  // for the drain: full barriers with a copy started, and their last phase
   int issued;              // some MMA was issued
   alignas(16) float xs[kLinEpi][kLinMaxN / 2];     // token scales of the epilogue warps' columns
   int pre[kLinMaxE + 1];   // row tiles before each expert
@@ -552,15 +539,16 @@ __device__ __forceinline__ bool lin_wait_acc(const LinArgs &a, LinBars *b, int b
 
 // After a wait gave up and every role has left: copies and MMAs that were started end before the
 // CTA frees its tensor memory and exits.  (Without a failure the epilogue's waits have seen to it.)
-// OWN: every CTA's barriers count its own copies.
+// full: the `n` barriers of the copies; OWN: every CTA's count its own.
 template <bool PAIR, bool OWN = !PAIR>
-__device__ __noinline__ void lin_drain(LinBars *b, int stages, uint32_t rank, int warp, int lane) {
+__device__ __noinline__ void lin_drain(LinBars *b, uint64_t *full, int n, uint32_t rank, int warp,
+                                       int lane) {
   if (warp == 0 && lane == 0) {
     // PAIR: the leader's barriers count both CTAs' copies; one that the second CTA had not started
     // is not worth a long wait
-    for (int q = 0; q < stages; q++)
+    for (int q = 0; q < n; q++)
       if ((b->armed >> q) & 1)
-        wait_nofail(&b->full[q], (b->phases >> q) & 1, OWN ? kLinWaitNs : kLinLateNs);
+        wait_nofail(&full[q], (b->phases >> q) & 1, OWN ? kLinWaitNs : kLinLateNs);
     // the second CTA of a pair has no barrier of its own to wait on: its copies are loads of
     // some microseconds
     if (!OWN && rank) for (int i = 0; i < 1000; i++) __nanosleep(1000);

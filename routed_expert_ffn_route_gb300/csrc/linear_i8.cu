@@ -26,9 +26,7 @@ namespace moe {
 
 constexpr int kI8Threads = kLinThreads + 256;
 constexpr int kI8Set = 4;     // converter warps of a set; two sets
-constexpr int kI8Slots = 4;   // fp16 sub-blocks on their way to the MMA
 constexpr int kI8Exact = 16;  // sub-blocks (1024 products) summed in tensor memory: exact
-constexpr int kI8MaxN = 192;  // token rows per tile
 // Tensor memory: two accumulators, then the weights' sub-blocks, 32 columns each.  (Eight slots, where
 // the accumulators are narrow: no gain.)
 constexpr int kI8A = 2 * kI8MaxN;
@@ -39,8 +37,23 @@ constexpr int kI8Acc = lin_exact<TO> ? kLinAcc<TO> : kI8MaxN;
 struct I8Args : LinArgs {
   int conv;  // bytes of a token sub-block; kI8Slots of them behind the raw stages
 };
-struct I8Bars : LinBars {  // full, empty: of this CTA's raw stages
+// empty: of this CTA's raw stages.  raw_full: two barriers a stage, which its k-blocks take in turn
+// (LinBars' full is not used).  A wait tests one parity bit and cannot tell a phase from the one two
+// before it.  With one barrier and an odd number of stages, a set comes to stages whose last k-block
+// was the other set's: where that has not landed, the wait passes at once (three stages; with five and
+// more the wait for the slots holds the set back).  With two, k-block i shares its barrier with k-block
+// i + 2 stages, an even number on, so that one set waits for every phase of it.
+struct I8Bars : LinBars {
+  uint64_t raw_full[2][kLinStages];
   uint64_t conv_full[kI8Slots], conv_empty[kI8Slots];
+};
+// place in a ring of raw stages: the stage, which of its barriers, and the parity of that one's phase
+struct I8Place {
+  int s = 0;
+  uint32_t lap = 0, ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) s = 0, ph ^= lap, lap ^= 1;
+  }
 };
 
 // Arrive in CTA `rank` of the cluster, for writes that the tensor cores read: they are the async
@@ -139,7 +152,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < a.stages; s++) {
-      tc::mbar_init(&b->full[s], 1);
+      tc::mbar_init(&b->raw_full[0][s], 1);
+      tc::mbar_init(&b->raw_full[1][s], 1);
       tc::mbar_init(&b->empty[s], kI8Set);
     }
     for (int s = 0; s < kI8Slots; s++) {
@@ -182,26 +196,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // ---------------------------------------------- producer: raw stages of this CTA
       bool ok = true;
       uint32_t armed = 0, last_ph = 0;
-      int s = 0;
-      uint32_t ph = 0;
+      I8Place p;
       for (int tile = cta; tile < total && ok; tile += ctas) {
         const LinTile t = lin_tile(a, b, tile);
         const int ft = PAIR ? 2 * t.ft + rank : t.ft;
         // the pair's MMAs take the first half of the columns from the leader
         const int row = t.r0 + (PAIR ? (int)rank * (round16(t.n) / 2) : 0);
         for (int kb = kb0; kb < kb1; kb++) {
-          if (!tc::mbar_wait(&b->empty[s], ph ^ 1, abort, kLinWaitNs)) { ok = false; break; }
-          uint8_t *st = ring + (size_t)s * stage_bytes;
-          const uint32_t bar = tc::smem_u32(&b->full[s]);
-          tc::mbar_arrive_expect_tx(&b->full[s], stage_bytes);
-          armed |= 1u << s;
-          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          if (!tc::mbar_wait(&b->empty[p.s], p.lap ^ 1, abort, kLinWaitNs)) { ok = false; break; }
+          uint8_t *st = ring + (size_t)p.s * stage_bytes;
+          const int full = (int)p.lap * kLinStages + p.s;
+          const uint32_t bar = tc::smem_u32(&b->raw_full[0][full]);
+          tc::mbar_arrive_expect_tx(&b->raw_full[0][full], stage_bytes);
+          armed |= 1u << full;
+          last_ph = (last_ph & ~(1u << full)) | (p.ph << full);
           if (GATED)
             lin_load_5d<false>(st, &wmap, bar, kb * a.ke, ft * (kLinM / 32), t.e);
           else
             lin_load_3d<false>(st, &wmap, bar, kb * a.ke, ft * kLinM, t.e);
           lin_load_2d<false>(st + kLinM * 128, &xmap, bar, kb * a.ke, row);
-          if (++s == a.stages) s = 0, ph ^= 1;
+          p.next(a.stages);
         }
       }
       b->armed = armed;
@@ -266,18 +280,19 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int set = (warp - 2 - kLinEpi) / kI8Set, quad = warp & 3;  // the warp's quarter of the rows
     const uint32_t ta = tbase + ((uint32_t)(32 * quad) << 16) + kI8A;
     bool ok = true;
-    int s = 0;
-    uint32_t ph = 0, turn = 0, cph = 0;
+    I8Place p;
+    uint32_t turn = 0, cph = 0;
     for (int tile = cta; tile < total && ok; tile += ctas) {
       const LinTile t = lin_tile(a, b, tile);
       // token rows that the MMAs read from here
       const int groups = (PAIR ? round16(t.n) / 2 : round16(t.n)) / 8;
       for (int kb = kb0; kb < kb1; kb++, turn ^= 1) {
         if (turn == set) {
-          if (!__all_sync(0xffffffffu, tc::mbar_test_wait(&b->full[s], ph)))
-            ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(&b->full[s], ph, abort, kLinWaitNs));
+          uint64_t *const full = &b->raw_full[p.lap][p.s];
+          if (!__all_sync(0xffffffffu, tc::mbar_test_wait(full, p.ph)))
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(full, p.ph, abort, kLinWaitNs));
           if (!ok) break;
-          const uint8_t *raw = ring + (size_t)s * stage_bytes;
+          const uint8_t *raw = ring + (size_t)p.s * stage_bytes;
           const uint8_t *wraw = raw + quad * 32 * 128, *xraw = raw + kLinM * 128 + quad * 1024;
 #pragma unroll
           for (int h = 0; h < 2; h++) {  // the block's two sub-blocks
@@ -309,7 +324,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              if (h) tc::mbar_arrive(&b->empty[s]);
+              if (h) tc::mbar_arrive(&b->empty[p.s]);
               if (PAIR) i8_arrive_in_cta(&b->conv_full[c], 0);
               else tc::mbar_arrive(&b->conv_full[c]);
             }
@@ -317,7 +332,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           if (!ok) break;
           cph ^= 1;
         }
-        if (++s == a.stages) s = 0, ph ^= 1;
+        p.next(a.stages);
       }
     }
     if (!ok && lane == 0) lin_give_up<PAIR>(a, b, rank);
@@ -337,7 +352,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (PAIR) cluster_sync(); else __syncthreads();  // nobody still uses a peer's barriers
   tc::fence_after_sync();
   if (*abort) {  // the same for all threads: every role has left
-    lin_drain<PAIR, true>(b, a.stages, rank, warp, lane);
+    lin_drain<PAIR, true>(b, b->raw_full[0], 2 * kLinStages, rank, warp, lane);
     tc::fence_before_sync();
     if (PAIR) cluster_sync(); else __syncthreads();
     tc::fence_after_sync();
@@ -350,18 +365,6 @@ static size_t i8_smem(int bytes) {  // of the rings and the exchange
   const int more = 1024 + (int)sizeof(I8Bars) + (MODE == kSplit ? 0 : kLinStage);
   set_dyn_smem((const void *)linear_i8_kernel<TO, GATED, MODE>, kLinRing + more);
   return bytes + more;
-}
-
-// columns of a split tile that one CTA finishes, and the bytes of the partial sums' exchange
-static int i8_exchange(int BN, int split) {
-  const int cpc = ((BN + split - 1) / split + 3) & ~3;
-  return split * cpc * kLinM * 4;
-}
-
-// raw stages beside the exchange and the token sub-blocks of xrows rows
-static int i8_stages(int xrows, int exchange) {
-  return std::min(kLinStages,
-                  (kLinRing - exchange - kI8Slots * xrows * 128) / ((kLinM + xrows) * 128));
 }
 
 static int i8_clusters(int split) {
@@ -388,63 +391,6 @@ static int i8_clusters(int split) {
   });
 }
 
-struct I8Plan {
-  int mode, BN, split;
-  long tiles;
-  bool sure;  // made with every answer
-};
-
-// How to cut the product: an estimate in SM cycles of each candidate.  A k-block of 128 takes as long as
-// its MMAs (4 cycles a column), 800 cycles (a hand-over and eight MMAs take no less), or the rows that
-// are turned into fp16 (3.5 cycles each), whichever is longest; joining a split tile takes 2000 cycles and
-// 12 a column and other CTA.  Over 16 shapes (64 to 32768 rows, 1024 to 8192 features, K 1024 to 14336,
-// 0 to 64 experts) the form taken is 2% slower than the fastest of six widths in every mode in the
-// mean, 11% at worst (4096 rows of 64 experts: one CTA a tile 348 us, a pair 313).
-static I8Plan i8_make_plan(int R, int N, int E, int KB, bool gated, bool exact) {
-  const int sms = dev_info().sms;
-  // experts that get rows, and rows of one of them, when rows fall on experts evenly
-  const double active = E > 1 ? E * (1.0 - std::pow(1.0 - 1.0 / E, R)) : 1.0;
-  const double m = R / active;
-  const int rows = gated ? 2 * N : N;
-  const int clusters[3] = {i8_clusters(2), i8_clusters(4), i8_clusters(8)};
-  I8Plan best{};
-  best.sure = clusters[0] > 0 && clusters[1] > 0 && clusters[2] > 0;
-  double cost = 1e30;
-  for (int mode = 0; mode < 3; mode++)
-    for (int BN = 16; BN <= kI8MaxN; BN += 16)
-      for (int split = mode == kSplit ? 2 : 1; split <= (mode == kSplit ? 8 : 1); split *= 2) {
-        if (mode == kPair && (BN < 64 || BN % 32 || rows <= kLinM)) continue;
-        if (split > KB) continue;
-        if (exact && (mode == kPair || BN > (mode == kSplit ? kLinExactSplitN : kLinExactN)))
-          continue;
-        const int FT = (rows + (mode == kPair ? 255 : 127)) / (mode == kPair ? 256 : 128);
-        const double rt = E ? std::max(1.0, m / BN + 0.5) : (double)((R + BN - 1) / BN);
-        const double tiles = active * rt * FT;
-        const double cols = std::min((double)BN, m);
-        const double x = mode == kPair ? cols / 2 : cols;
-        const double kb = std::max({4.0 * cols, 800.0, 3.5 * (kLinM + x)});
-        double c;
-        if (mode == kSplit) {  // one tile a cluster
-          if (tiles > clusters[split == 2 ? 0 : split == 4 ? 1 : 2]) continue;
-          if (i8_stages(BN, i8_exchange(BN, split)) < 2) continue;
-          c = (KB + split - 1) / split * kb + 2000 + 12.0 * BN * (split - 1);
-        } else {
-          const double width = mode == kPair ? sms / 2 : sms;
-          const double waves = E ? std::max(1.0, tiles / width + 0.3) : std::ceil(tiles / width);
-          c = waves * KB * kb + 500 + 4.0 * BN;  // the last tile's epilogue
-        }
-        if (c < cost * 0.999) {
-          cost = c;
-          best.mode = mode, best.BN = BN, best.split = split;
-        }
-      }
-  const int FT = (rows + (best.mode == kPair ? 255 : 127)) / (best.mode == kPair ? 256 : 128);
-  // at most so many tiles exist, however the rows fall on the experts
-  const long rt = E ? (long)std::min(R, E) + R / best.BN : (R + best.BN - 1) / best.BN;
-  best.tiles = rt * FT;
-  return best;
-}
-
 // the plans of the last sizes seen by this thread (the estimate costs about a launch)
 static I8Plan i8_plan(int R, int N, int E, int KB, bool gated, bool exact) {
   struct Entry {
@@ -460,7 +406,8 @@ static I8Plan i8_plan(int R, int N, int E, int KB, bool gated, bool exact) {
   Entry &e = seen[(h >> 16) & 63];
   if (e.R == R && e.N == N && e.E == E && e.KB == KB && e.form == form && e.dev == dev)
     return e.plan;
-  const I8Plan plan = i8_make_plan(R, N, E, KB, gated, exact);
+  const int clusters[3] = {i8_clusters(2), i8_clusters(4), i8_clusters(8)};
+  const I8Plan plan = i8_make_plan(R, N, E, KB, gated, exact, dev_info().sms, clusters);
   if (plan.sure) e = Entry{R, N, E, KB, form, dev, plan};
   return plan;
 }

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (a.E && warp >= 2) lin_zero_rows<TO>(a, b, tid);
   __syncwarp();
   __syncthreads();
-  if (*abort) lin_drain<false, true>(b, a.stages, 0, warp, lane);
+  if (*abort) lin_drain<false, true>(b, b->full, a.stages, 0, warp, lane);
 }
 
 template <typename TO, bool GATED, int MR, int NT>
