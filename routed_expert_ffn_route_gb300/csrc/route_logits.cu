@@ -304,8 +304,10 @@ __device__ __noinline__ int route_near(const RouteArgs &a, const T *row, uint32_
       const int e = V * from + __shfl_sync(0xffffffffu, at, from);
       const float x = route_value(last), y = route_value(best);
       if (a.bias && n > 0 && x - y <= eps + 0x1p-21f * fabsf(x)) {
-        if (n >= a.k) {
-          // equal logits with equal biases stay behind the one that was found first
+        if (n >= a.k && !near) {
+          // Equal logits with equal biases stay behind the one that was found first, and without a
+          // different one near it that one stays where it is.  (With one it may move up past the last
+          // slot, and others with it: they are ranked too.)
           const float lp = fminf(route_f32(row[prev]), FLT_MAX), bp = a.bias[prev];
           bool same = best == last;
 #pragma unroll
