@@ -148,6 +148,14 @@ __device__ __forceinline__ void route_scores(const RouteArgs &a, const float (&l
 // exponential, sum and division; a sigmoid's slope is 1/4.
 __device__ __forceinline__ float route_eps(int softmax) { return softmax ? 0x1p-18f : 0x1p-20f; }
 
+// The largest finite |score| of all groups, from the lane's group's two best.  With a bias the scores
+// round as they are large, and so do the sums of two of both signs, however small those come out; and a
+// group far from the border may be off by more than the two at it.
+__device__ __forceinline__ float route_largest(float m1, float m2) {
+  const float x = fabsf(m1) < INFINITY ? fabsf(m1) : 0.f, y = fabsf(m2) < INFINITY ? fabsf(m2) : 0.f;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(x, y))));
+}
+
 template <int V>
 __device__ __forceinline__ void route_bias(const RouteArgs &a, int lane, float (&b)[V]) {
   if (V >= 4 && a.vec && a.bias && V * lane < a.E) {
@@ -175,9 +183,8 @@ __device__ __noinline__ uint32_t route_groups(const RouteArgs &a, const T *row, 
   for (int v = 0; v < V; v++)
     if (V * lane + v < a.E) fbuf[V * lane + v] = c[v];
   __syncwarp();
-  float s = -INFINITY;  // lane g: group g
+  float s = -INFINITY, m1 = -INFINITY, m2 = -INFINITY;  // lane g: group g
   if (lane < a.G) {
-    float m1 = -INFINITY, m2 = -INFINITY;
     for (int i = 0; i < gs; i++) {
       const float x = fbuf[lane * gs + i];
       m2 = fmaxf(m2, fminf(m1, x));
@@ -192,7 +199,8 @@ __device__ __noinline__ uint32_t route_groups(const RouteArgs &a, const T *row, 
     const uint32_t out = __ballot_sync(0xffffffffu, lane < a.G && rank == a.keep);
     const float si = __shfl_sync(0xffffffffu, s, __ffs(in) - 1);
     const float so = __shfl_sync(0xffffffffu, s, __ffs(out) - 1);
-    if (so > -INFINITY && si - so <= 2.f * route_eps(a.softmax) + 0x1p-21f * fabsf(si)) {
+    const float big = route_largest(m1, a.best == 2 ? m2 : 0.f);
+    if (so > -INFINITY && si - so <= 2.f * route_eps(a.softmax) + 0x1p-21f * big) {
       double total64 = 1.0;
       if (a.softmax) {
         total64 = 0.0;
@@ -435,12 +443,14 @@ __device__ __forceinline__ bool two_less(Two a, Two b) { return a.h < b.h || (a.
 
 // The rank of the lane's group where the last one kept (score si) and the first one left out (so)
 // lie within `tol`: those groups' scores in two floats, from the experts that may be among their
-// two best, one a lane.  near: that does not tell them apart either.  mem: 96 words of this warp.
+// two best, one a lane.  big: the largest score that a sum is made of, 0 without a bias.  near: that
+// does not tell them apart either.  mem: 96 words of this warp.
 template <int V>
 __device__ __noinline__ int route_groups_two(const RouteArgs &a, const float (&l)[V],
                                              const float (&b)[V], const float (&c)[V], float top,
                                              float s, float m1, float m2, float si, float so,
-                                             float tol, int rank, int lane, float *mem, bool &near) {
+                                             float tol, float big, int rank, int lane, float *mem,
+                                             bool &near) {
   const bool close = s >= so - tol && s <= si + tol;
   const float least = (a.best == 2 && m2 > -INFINITY ? m2 : m1) - 2.f * tol;
   const int g = lane >> a.shift;
@@ -477,7 +487,8 @@ __device__ __noinline__ int route_groups_two(const RouteArgs &a, const float (&l
     if (both) {
       const float d = (oh - sum.h) + (ol - sum.l);
       r += d > 0.f;
-      near |= q != g && !(fabsf(d) > (a.softmax ? 0.f : 0x1p-35f) + 0x1p-35f * fabsf(sum.h));
+      near |= q != g && !(fabsf(d) > (a.softmax ? 0.f : 0x1p-35f) + 0x1p-35f * fabsf(sum.h) +
+                                        0x1p-42f * big);
     } else {
       r += os > s || (os == s && q < g);
     }
@@ -571,8 +582,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_logits_kernel(const
         const float so = __shfl_sync(0xffffffffu, s, __ffs(out) - 1);
         // without a bias a softmax's errors go with its size: the exponential's argument is off by
         // up to 88 u, and its smallest results by their last bits
+        const float big = BIAS ? route_largest(m1, a.best == 2 ? m2 : 0.f) : 0.f;
         const float tol = a.softmax && !BIAS ? 0x1p-16f * si + 0x1p-120f
-                                             : eps + 0x1p-21f * fabsf(si);
+                                             : eps + 0x1p-21f * (BIAS ? big : si);
         if (so > -INFINITY && si - so <= tol) {
           near = BIAS && a.softmax;
           if (!near) {
@@ -580,8 +592,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) route_logits_kernel(const
 #pragma unroll
             for (int v = 0; v < V; v++) l2[v] = l[v], b2[v] = b[v], c2[v] = c[v];
             bool near2 = false;
-            rank = route_groups_two<V>(a, l2, b2, c2, top, s, m1, m2, si, so, tol, rank, lane,
-                                       (float *)buf[warp], near2);
+            rank = route_groups_two<V>(a, l2, b2, c2, top, s, m1, m2, si, so, tol, big, rank,
+                                       lane, (float *)buf[warp], near2);
             near = near2;
           }
         }
