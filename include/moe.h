@@ -385,7 +385,8 @@ int moe_route_logits_grad(int T, int n_experts, int k, const float *dw, const vo
  *   q [R][2 I] e4m3 codes of z and scale [R][2 ceil(I / group)] fp32, the gate's groups of `group`
  *   columns (32, 64, 128 or 256, the last one may be shorter), then the up columns': scale =
  *   max|z| / 448, q = e4m3(z * 448 / max|z|), with moe_rmsnorm_e4m3's rules for zeros, NaN and
- *   infinities.  Sums and products are fp32, each output is rounded once.  I <= 2^24. */
+ *   infinities.  Sums and products are fp32, each output is rounded once; silu(gate) of a gate
+ *   below -87, of 2^-119 and less, may be 0.  I <= 2^24. */
 int moe_swiglu_e4m3(int R, int I, const void *z, long ldz, moe_dtype dtype, int group, void *h,
                     long ldh, uint8_t *q, long ldq, float *scale, void *stream);
 
@@ -410,7 +411,8 @@ int moe_swiglu_e4m3_grad(int R, int I, const void *dh, long lddh, moe_dtype dtyp
  * Accumulation is fp32 on the tensor cores, whose sums are truncated; for F32 outputs they are
  * added up in registers every few hundred of K, rounded to nearest.  I8: codes and scales as
  * moe_quantize_rows (bits = 8) makes them; sums are whole numbers, exact up to 2^24, and for F32
- * outputs exact over every 1024 of K.  x, w and (R > 1) x's rows
+ * outputs exact over every 1024 of K; for 16-bit outputs each 16 of K past 2^24 cuts off at most
+ * 2^-23 of the sum so far (in all at most K 2^-27 of the products' magnitudes).  x, w and (R > 1) x's rows
  * 16-byte aligned; K a multiple of 16, N of 16 for SWIGLU, E <= 256, else MOE_ERR_UNSUPPORTED.
  * status: optional device int32, set to MOE_ERR_TIMEOUT if a bounded wait gave up (the output is
  * then undefined), else left as it is. */

@@ -640,8 +640,8 @@ __device__ __forceinline__ void lin_offsets(const LinArgs &a, LinBars *b, int wa
 template <typename TO>
 using H16 = std::conditional_t<sizeof(TO) == 2, TO, __half>;
 
-// The tiles of one epilogue warp.  acc: columns between the accumulators (EXACT: kLinAcc<float>).  The scales and biases of the next tile are loaded while this
-// one is worked on.
+// The tiles of one epilogue warp.  acc: columns between the accumulators (EXACT: kLinAcc<float>).  The
+// scales and biases of the next tile are loaded while this one is worked on.
 template <typename OUT, bool PAIR, bool EXACT, int CHUNK = kLinExact>
 __device__ __forceinline__ void lin_epilogue(const LinArgs &a, LinBars *b, uint32_t tbase, int tile,
                                              int ctas, int total, int kblocks, int acc,

@@ -457,7 +457,10 @@ static int launch_i8_t(const CUtensorMap &xm, const CUtensorMap &wm, const I8Arg
 }
 
 // Whether the form for few rows (linear_i8_few.cu) takes the product.  Its MMAs keep up with memory
-// for 8 token rows a tile, and take twice as long for 16.
+// for 8 token rows a tile, and take twice as long for 16.  That was measured where there are about as
+// many tiles as SMs, 2048 features and more; fewer features are bound by what one SM reads of K
+// (one row: 256 to 1024 features of K = 6144 4.9 to 5.0 us, of 14336 7.5 to 7.7).  With several experts:
+// five rows an expert in the mean.
 static bool i8_few(int R, int rows, int K, int E) {
   if (E <= 1) return R <= 8 || (R <= 16 && (long)rows * K <= 24 << 20);
   return R <= 5.0 * E * (1.0 - std::pow(1.0 - 1.0 / E, R));

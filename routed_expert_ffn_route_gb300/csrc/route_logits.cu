@@ -10,8 +10,11 @@
 // that a lower lane means a lower index and a group is a run of lanes.  Scores become integers of
 // the same order whose last bits give way to the place in the lane; each lane sorts its own, and
 // the k largest come out one after the other: the warp's largest by one reduction, the first lane
-// that holds it gives it up.  8192 tokens of 256 experts: 6.2 us without a bias, 10.3 with one and eight
-// groups, of which 2.2 are a launch; bound by instructions, some 550 and 850 a token.
+// that holds it gives it up.  8192 tokens of 256 experts: 6.2 us without a bias, sigmoid with one 8.4,
+// with one and eight groups 10.3, of which 2.2 are a launch; bound by instructions, some 550 (no
+// bias) and 850 (groups) a token.  Two forms take longer: softmax with a bias, whose near scores go
+// to fp64 (23 us, 32 in eight groups; 64 experts 12), and groups that are no run of 2^n lanes, which
+// one lane each walks (8192 x 160 in eight groups: sigmoid with a bias 23 us, softmax 35).
 //
 // What is chosen is what 64-bit scores choose.  Without a bias the logits themselves have the
 // scores' order.  With one, fp32 scores are compared, and where two that follow each other lie
@@ -523,7 +526,8 @@ __device__ __forceinline__ void route_sort(uint32_t (&v)[V]) {
 // BIAS: the choice goes by scores with a bias, else by the logits.  (The arguments stay in constant
 // memory: calls take their address, for which every thread otherwise copies them to its stack.)
 template <typename T, int V, bool BIAS>
-__global__ void __launch_bounds__(32 * kRouteWarps, 8) route_logits_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps, 8)
+    route_logits_kernel(const __grid_constant__ RouteArgs a) {
   __shared__ double buf[kRouteWarps][kRouteMaxE];
   pdl_wait();
   pdl_trigger();

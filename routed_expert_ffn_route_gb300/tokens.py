@@ -121,7 +121,8 @@ def moe_route_logits(logits, ids, w, bias=None, router="softmax", n_group=1, top
 
 def moe_route_logits_grad(dw, logits, ids, dlogits, router="softmax", norm_topk=True,
                           routed_scaling_factor=1.0, stream=None):
-    """dlogits [T, E] of dw [T, k], for the ids that moe_route_logits chose."""
+    """dlogits [T, E] of dw [T, k], for the ids that moe_route_logits chose; dlogits is not the logits'
+    own memory."""
     _check(_native.route_logits_grad(dw, logits, ids, dlogits, _router(router), norm_topk,
                                      routed_scaling_factor, stream), "moe_route_logits_grad")
 
