@@ -132,6 +132,16 @@ __device__ __forceinline__ float slots_max(float v) {
   return v;
 }
 
+// What the slots' scores are to each other, one a lane (0 of -inf): exp(x), or sigmoid(x), over exp(L),
+// with L the largest logit (sigmoid: or 0, where that is less).  Sigmoids of logits far below 0 are
+// their exponentials, and share out what no fp32 holds; rows with a deep one take this form.
+__device__ __forceinline__ bool route_deep(float x) { return x > -INFINITY && x < -60.f; }
+__device__ __forceinline__ float route_share(float x, int softmax) {
+  const float top = fmaxf(slots_max(x), -FLT_MAX);
+  if (softmax) return expf(x - top);
+  return expf(fminf(x, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(x)));
+}
+
 // The lane's scores with bias, unavailable ones -inf, from its logits and biases.  top, total:
 // softmax's largest logit and the sum of its exponentials.
 template <int V>
@@ -715,13 +725,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8)
   if (lane >= a.k) id = -1, x = -INFINITY;
   float s;
   if (a.norm) {
-    // sigmoids of logits far below 0 are their exponentials, and share out what no fp32 holds
-    if (a.softmax || !__any_sync(0xffffffffu, x >= -60.f)) {
-      const float L = fmaxf(slots_max(x), -FLT_MAX);
-      s = expf(x - L);
-    } else {
+    if (a.softmax || __any_sync(0xffffffffu, route_deep(x)))
+      s = route_share(x, a.softmax);
+    else
       s = 1.f / (1.f + expf(-x));  // 0 of -inf
-    }
     s /= fmaxf(slots_sum(s), FLT_MIN);  // (none is chosen: 0)
   } else {
     s = a.softmax ? expf(x - top) / total : 1.f / (1.f + expf(-x));
@@ -832,8 +839,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const Rout
     if (total == 0.f) total = 1.f;  // no expert is available: every term is 0
   }
   float s, rest = 1.f;  // the score (0 of -inf), and 1 - a sigmoid
-  if (a.norm && (a.softmax || !__any_sync(0xffffffffu, x >= -60.f)))
-    s = expf(x - fmaxf(slots_max(x), -FLT_MAX));
+  if (a.norm && (a.softmax || __any_sync(0xffffffffu, route_deep(x))))
+    s = route_share(x, a.softmax);
   else
     s = a.softmax ? expf(x - top) / total : 1.f / (1.f + expf(-x));
   if (!a.softmax) rest = 1.f / (1.f + expf(x));
