@@ -416,13 +416,17 @@ __device__ __forceinline__ Two two_of(double v) {  // of a constant
 }
 
 // sigmoid(l) + b, off by at most 2^-38 + 2^-46 |b|, or (softmax, without a bias) exp(l - top), by
-// 2^-38 of it.  exp(x) = 2^n exp(r) with |r| <= 0.35, whose Taylor series is summed in fp32 from the
-// fifth power on (which is below 2^-14, so that its rounding is below 2^-38) and in two floats before.
+// 2^-38 of it where l lies within kTwoDepth of top, and else that of the depth.  exp(x) = 2^n exp(r) with
+// |r| <= 0.35, whose Taylor series is summed in fp32 from the fifth power on (which is below 2^-14, so
+// that its rounding is below 2^-38) and in two floats before.
+constexpr float kTwoDepth = 80.f;
 __device__ __noinline__ Two route_two(float l, float b, int softmax, float top) {
   constexpr double kLn2 = 0.693147180559945309417;
   constexpr float kL1 = (float)((int)(kLn2 * 32768.0)) / 32768.0f;  // times n: exact
   constexpr float kL2 = (float)(kLn2 - kL1), kL3 = (float)(kLn2 - kL1 - kL2);
-  const Two x = softmax ? two_sum(fmaxf(l, top - 80.f), -top) : Two{-fminf(fabsf(l), 80.f), 0.f};
+  const Two x = !softmax               ? Two{-fminf(fabsf(l), kTwoDepth), 0.f}
+                : l - top < -kTwoDepth ? Two{-kTwoDepth, 0.f}
+                                       : two_sum(l, -top);
   const float n = rintf(x.h * 1.44269504f);
   const float t = __fmaf_rn(-n, kL1, x.h);  // exact
   const float p = __fmul_rn(n, kL2), pe = __fmaf_rn(n, kL2, -p);
@@ -480,6 +484,9 @@ __device__ __noinline__ int route_groups_two(const RouteArgs &a, const float (&l
   if (near) return rank;
   __syncwarp();
   const bool have = lane < n;
+  // a softmax's scores below the depth would all count as one size, and their number decide
+  near = a.softmax && __any_sync(0xffffffffu, have && mem[lane] - top < -kTwoDepth);
+  if (near) return rank;
   const Two x = route_two(have ? mem[lane] : top, have ? mem[32 + lane] : 0.f, a.softmax, top);
   const int of = have ? (int)mem[64 + lane] : -1;
   __syncwarp();
