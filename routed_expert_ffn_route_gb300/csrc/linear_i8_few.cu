@@ -16,7 +16,7 @@
 //
 // Measured: one row of 6144 x 2048 5.2 us (clusters that split K, linear_i8.cu: 10.9); 8 rows of
 // 4096 x 155648 96 us, weights at 6.6 TB/s (16 rows: 163, linear_i8.cu 113); 128 rows of 64 experts
-// (6144 x 2 x 2048) 197 to 215 us (250 to 270).
+// (6144 x 2 x 2048) 197 to 220 us (250 to 270).
 #include "linear.cuh"
 
 namespace moe {
